@@ -1,0 +1,75 @@
+// fg8_columns.cuh -- pieces of the kernels that quantize down the token axis
+// from 8-bit inputs (act_backward.cu, requant.cu).
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "fg8_common.cuh"
+
+namespace fg8 {
+
+constexpr int kColsMaxE = 1024;
+
+// Two E4M3 codes (bits 7..0 and 15..8) -> fp32, exact.
+FG8_DEV float2 e4m3x2_f32(uint32_t codes) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// The scale of a tile of fp32 values without the division routine: q = amax /
+// 448 from the rounded reciprocal and one residual correction, the IEEE quotient
+// for every amax >= 2^-110 (checked over all of them); below that the division.
+FG8_DEV float tile_scale_fast(float amax) {
+    if (amax < 0x1p-110f) return tile_scale32(amax);
+    const float r = 1.0f / 448.0f;
+    const float q = __fmul_rn(amax, r);
+    return __fmaf_rn(__fmaf_rn(-q, 448.0f, amax), r, q);
+}
+
+// A code factor for scale s: E4M3(x * inv_scale(s)) is x / s rounded with a
+// relative error of 2^-22 before the rounding to 4 bits.  Subnormal scales
+// (amax < 448 * 2^-126) have no finite fp32 reciprocal: callers divide there.
+FG8_DEV float inv_scale(float s) {
+    float r0;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r0) : "f"(s));
+    return __fmaf_rn(r0, __fmaf_rn(-s, r0, 1.0f), r0);
+}
+FG8_DEV bool scale_subnormal(float s) { return !(s >= 1.17549435e-38f); }
+
+// One 128-row tile of an expert in the padded token axis.
+struct RowTile {
+    int64_t row0;   // first logical row
+    int n_in;       // rows of the expert in it (>= 1, <= 128)
+    int64_t pcol;   // first padded column
+};
+
+// s_pref: exclusive prefix of tiles per expert (s_pref[E] = all tiles);
+// offsets as the caller gave them; R rows exist.
+FG8_DEV RowTile find_tile(int tile, const int32_t* s_pref, const int32_t* offsets, int E, int64_t R) {
+    int lo = 0, hi = E;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_pref[mid] <= tile) lo = mid; else hi = mid;
+    }
+    const int tb = tile - s_pref[lo];
+    const int32_t o0 = offsets[lo], o1 = offsets[lo + 1];
+    RowTile t;
+    t.row0 = (int64_t)o0 + 128 * (int64_t)tb;
+    // rows that the buffers do not hold (offsets inconsistent with R) are not touched
+    t.n_in = (int)max((int64_t)0, min((int64_t)min(128, o1 - o0 - 128 * tb), R - t.row0));
+    if (t.row0 < 0) t.n_in = 0;
+    t.pcol = (int64_t)128 * tile;
+    return t;
+}
+
+// Tiles per expert -> s_pref (exclusive prefix, s_pref[E] = total), by all
+// threads of the block; s_warp: 33 words.
+FG8_DEV void tile_prefix(const int32_t* offsets, int E, int32_t* s_pref, int32_t* s_warp) {
+    for (int e = threadIdx.x; e < E; e += blockDim.x)
+        s_pref[e] = (max(0, offsets[e + 1] - offsets[e]) + 127) / 128;
+    __syncthreads();
+    block_exclusive_scan(s_pref, s_pref, E, s_warp);
+}
+
+}  // namespace fg8

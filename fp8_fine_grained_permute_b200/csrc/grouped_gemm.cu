@@ -42,6 +42,10 @@
 // accumulates the gate and warpgroup 1 the up projection; after the last K
 // block the up values are handed to the gate warps through TMEM and the
 // epilogue writes silu(gate) * up as E4M3 codes with one scale per 1x128 tile.
+// Saving variant (fg8_grouped_gemm_swiglu_quant_save): each warpgroup first
+// writes its own half, the gate or the up projection, as 1x128 E4M3 tiles from
+// the fp32 accumulators -- the 8-bit checkpoint of the activation's inputs.  A
+// thread owns a row, so a tile's maximum needs no exchange.
 //
 // Every mbarrier wait is bounded (FG8_ERR_TIMEOUT in *status, then the roles
 // wind down and TMEM is released); the kernel never traps.
@@ -174,6 +178,10 @@ struct GemmArgs {
     // 1x128 scales [I/128][M_total]
     int swiglu;
     float* out_scale;
+    // gate/up mode that saves: codes of [gate up] [M_total][2 I] and their 1x128
+    // scales [2 I / 128][M_total]
+    uint8_t* gu;
+    float* gu_scale;
     // row-grouped combine mode: out = fp32 [T][N] token rows, each routed row
     // added with its gate weight: row_tok[r], row_w[r] (fg8_grouped_gemm_combine)
     const int32_t* row_tok;
@@ -401,7 +409,7 @@ FG8_DEV bool ring_take(TileRing& R, bool whole_warp, int4& v, volatile int* abor
 // the kernel
 // ---------------------------------------------------------------------------
 
-template <bool kGroupK, bool kSwiglu = false, bool kCombine = false>
+template <bool kGroupK, bool kSwiglu = false, bool kCombine = false, bool kSave = false>
 __global__ void __launch_bounds__(Warps<kGroupK>::kThreads, 1)
 grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                     const __grid_constant__ CUtensorMap tmB,
@@ -814,6 +822,47 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                 const uint32_t lb = tmem_base + ((uint32_t)(32 * quarter) << 16) + lbuf * BN;
                 const uint32_t xp = (xphase >> lbuf) & 1u;
                 xphase ^= 1u << lbuf;
+                // 64 codes of this thread's row (float2 first..first + 31 of acc)
+                // through the warp's staging rows: each store writes 8 rows x 64
+                // bytes, to rows of `pitch` bytes at `base`
+                auto store_codes64 = [&](int first, const fg8::QScale& q, uint8_t* base, int64_t pitch) {
+                    uint32_t* stg = reinterpret_cast<uint32_t*>(smem + kOffStage) + ep * 32 * kStageWords;
+                    uint4* my_row = reinterpret_cast<uint4*>(stg + lane * kStageWords);
+                    const int sub = ((lane >> 2) & 1) * 4 + (lane >> 3);
+                    const int quad = lane & 3;
+#pragma unroll
+                    for (int w4 = 0; w4 < 4; ++w4) {
+                        uint2 c[2];
+#pragma unroll
+                        for (int hh = 0; hh < 2; ++hh) {
+                            const int b = first + 8 * w4 + 4 * hh;   // float2 index: 8 values
+                            c[hh] = fg8::quant8f(acc[b], acc[b + 1], acc[b + 2], acc[b + 3], q);
+                        }
+                        my_row[w4] = make_uint4(c[0].x, c[0].y, c[1].x, c[1].y);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const int rr = 8 * g + sub;
+                        const uint4 v = *reinterpret_cast<const uint4*>(stg + rr * kStageWords + 4 * quad);
+                        if (32 * quarter + rr < rows_valid)
+                            *reinterpret_cast<uint4*>(base + (int64_t)(out_row0 + 32 * quarter + rr) * pitch +
+                                                      16 * quad) = v;
+                    }
+                    __syncwarp();
+                };
+                if (kSave) {   // the checkpoint: this warpgroup's 128 columns as they are
+                    float m = 0.f;
+#pragma unroll
+                    for (int i = 0; i < kCols / 2; ++i) m = fmaxf(m, fmaxf(fabsf(acc[i].x), fabsf(acc[i].y)));
+                    const float gsc = fg8::tile_scale32(m);
+                    const fg8::QScale gq = fg8::make_qscale(gsc);
+                    uint8_t* gb = a.gu + (grp ? a.N / 2 : 0) + col0;
+                    store_codes64(0, gq, gb, a.N);
+                    store_codes64(32, gq, gb + 64, a.N);
+                    if (row_ok)
+                        a.gu_scale[(int64_t)((grp ? a.N / 256 : 0) + col0 / 128) * a.M_total + out_row0 + r] = gsc;
+                }
                 if (grp == 0)
                     tmem_st64(lb + 64, acc + 32);
                 else
@@ -859,33 +908,8 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                 amax = fmaxf(amax, s_amax[(grp ^ 1) * BM + r]);
                 const float sc = fg8::tile_scale(amax);
                 const fg8::QScale q = fg8::make_qscale(sc);
-                // 64 codes of this thread's row through the warp's staging rows:
-                // each store writes 8 rows x 64 bytes
-                uint32_t* stg = reinterpret_cast<uint32_t*>(smem + kOffStage) + ep * 32 * kStageWords;
-                uint4* my_row = reinterpret_cast<uint4*>(stg + lane * kStageWords);
-                const int sub = ((lane >> 2) & 1) * 4 + (lane >> 3);
-                const int quad = lane & 3;
                 const int I = a.N / 2;
-                uint8_t* ob = static_cast<uint8_t*>(a.out) + col0 + 64 * grp + 16 * quad;
-#pragma unroll
-                for (int w4 = 0; w4 < 4; ++w4) {
-                    uint2 c[2];
-#pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
-                        const int base = 8 * w4 + 4 * hh;   // float2 index: 8 values
-                        c[hh] = fg8::quant8f(acc[base], acc[base + 1], acc[base + 2], acc[base + 3], q);
-                    }
-                    my_row[w4] = make_uint4(c[0].x, c[0].y, c[1].x, c[1].y);
-                }
-                __syncwarp();
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const int rr = 8 * g + sub;
-                    const uint4 v = *reinterpret_cast<const uint4*>(stg + rr * kStageWords + 4 * quad);
-                    if (32 * quarter + rr < rows_valid)
-                        *reinterpret_cast<uint4*>(ob + (int64_t)(out_row0 + 32 * quarter + rr) * I) = v;
-                }
-                __syncwarp();
+                store_codes64(0, q, static_cast<uint8_t*>(a.out) + col0 + 64 * grp, I);
                 if (grp == 0 && row_ok) a.out_scale[(int64_t)(col0 / 128) * a.M_total + out_row0 + r] = sc;
                 tc_fence_before();
                 __syncwarp();
@@ -1181,6 +1205,8 @@ extern "C" fg8_status fg8_grouped_gemm(const uint8_t* a, const float* sa, const 
     args.out_scale = nullptr;
     args.row_tok = nullptr;
     args.row_w = nullptr;
+    args.gu = nullptr;
+    args.gu_scale = nullptr;
     if (group_mode == FG8_GROUP_K) {
         args.ws = static_cast<unsigned int*>(workspace);
         if (cudaMemsetAsync(workspace, 0, kGroupKWorkspace, (cudaStream_t)stream) != cudaSuccess)
@@ -1193,11 +1219,11 @@ extern "C" fg8_status fg8_grouped_gemm(const uint8_t* a, const float* sa, const 
     return fg8h::launch_status();
 }
 
-extern "C" fg8_status fg8_grouped_gemm_swiglu_quant(const uint8_t* a, const float* sa,
-                                                    const uint8_t* b, const float* sb,
-                                                    const int32_t* offsets, int64_t M_total, int I,
-                                                    int K, int E, uint8_t* hq, float* sh,
-                                                    int32_t* dev_status, fg8_stream_t stream) {
+// The gate/up mode's launch; guq/sgu NULL: nothing is saved.
+static fg8_status launch_swiglu(const uint8_t* a, const float* sa, const uint8_t* b, const float* sb,
+                                const int32_t* offsets, int64_t M_total, int I, int K, int E,
+                                uint8_t* hq, float* sh, uint8_t* guq, float* sgu, int32_t* dev_status,
+                                fg8_stream_t stream) {
     if (!a || !sa || !b || !sb || !offsets || !hq || !sh) return FG8_ERR_INVALID_ARG;
     if (E < 1 || I < 128 || K < 128 || I % 128 || K % 128 || M_total < 0)
         return FG8_ERR_INVALID_ARG;
@@ -1216,7 +1242,7 @@ extern "C" fg8_status fg8_grouped_gemm_swiglu_quant(const uint8_t* a, const floa
     if (!make_map(&mA, a, (uint64_t)M_total, (uint64_t)K, BM) ||
         !make_map(&mB, b, (uint64_t)E * 2 * I, (uint64_t)K, 128))
         return FG8_ERR_CUDA;
-    auto kern = grouped_gemm_kernel<false, true>;
+    auto kern = guq ? grouped_gemm_kernel<false, true, false, true> : grouped_gemm_kernel<false, true>;
     cudaFuncAttributes fa;
     if (cudaFuncGetAttributes(&fa, (const void*)kern) != cudaSuccess) return FG8_ERR_CUDA;
     if (fa.numRegs < Warps<false>::kLaunchRegs) return FG8_ERR_UNSUPPORTED;
@@ -1240,12 +1266,34 @@ extern "C" fg8_status fg8_grouped_gemm_swiglu_quant(const uint8_t* a, const floa
     args.out_scale = sh;
     args.row_tok = nullptr;
     args.row_w = nullptr;
+    args.gu = guq;
+    args.gu_scale = sgu;
     int64_t grid = fg8h::num_sms();
     if (grid > max_tiles) grid = max_tiles;
     if (grid < 1) grid = 1;
     kern<<<(unsigned)grid, Warps<false>::kThreads, Layout<false>::kSmemBytes, (cudaStream_t)stream>>>(
         mA, mB, mA, args);
     return fg8h::launch_status();
+}
+
+extern "C" fg8_status fg8_grouped_gemm_swiglu_quant(const uint8_t* a, const float* sa,
+                                                    const uint8_t* b, const float* sb,
+                                                    const int32_t* offsets, int64_t M_total, int I,
+                                                    int K, int E, uint8_t* hq, float* sh,
+                                                    int32_t* dev_status, fg8_stream_t stream) {
+    return launch_swiglu(a, sa, b, sb, offsets, M_total, I, K, E, hq, sh, nullptr, nullptr, dev_status,
+                         stream);
+}
+
+extern "C" fg8_status fg8_grouped_gemm_swiglu_quant_save(const uint8_t* a, const float* sa,
+                                                         const uint8_t* b, const float* sb,
+                                                         const int32_t* offsets, int64_t M_total, int I,
+                                                         int K, int E, uint8_t* hq, float* sh,
+                                                         uint8_t* guq, float* sgu, int32_t* dev_status,
+                                                         fg8_stream_t stream) {
+    if (!guq || !sgu || !fg8h::aligned16(guq) || (reinterpret_cast<uintptr_t>(sgu) & 3))
+        return FG8_ERR_INVALID_ARG;
+    return launch_swiglu(a, sa, b, sb, offsets, M_total, I, K, E, hq, sh, guq, sgu, dev_status, stream);
 }
 
 extern "C" size_t fg8_grouped_gemm_combine_workspace(int64_t M_total) {
@@ -1316,6 +1364,8 @@ extern "C" fg8_status fg8_grouped_gemm_combine(const uint8_t* a, const float* sa
     args.out_scale = nullptr;
     args.row_tok = row_tok;
     args.row_w = row_w;
+    args.gu = nullptr;
+    args.gu_scale = nullptr;
     int64_t grid = fg8h::num_sms();
     if (grid > max_tiles) grid = max_tiles;
     if (grid < 1) grid = 1;

@@ -89,6 +89,19 @@ def lib() -> ctypes.CDLL:
         L.fg8_grouped_gemm_swiglu_quant.restype = _I
         L.fg8_grouped_gemm_swiglu_quant.argtypes = [_P, _P, _P, _P, _P, _I64, _I, _I, _I, _P, _P,
                                                     _P, _P]
+        L.fg8_grouped_gemm_swiglu_quant_save.restype = _I
+        L.fg8_grouped_gemm_swiglu_quant_save.argtypes = [_P, _P, _P, _P, _P, _I64, _I, _I, _I, _P,
+                                                         _P, _P, _P, _P, _P]
+        L.fg8_swiglu_backward_quant.restype = _I
+        L.fg8_swiglu_backward_quant.argtypes = [_P, _P, _P, _P, _P, _I64, _I, _I, _P, _P, _P, _P,
+                                                _P, _P, _P, _P, _P, _P]
+        L.fg8_requantize_colwise.restype = _I
+        L.fg8_requantize_colwise.argtypes = [_P, _P, _I64, _I64, _P, _P, _I64, _I, _P, _P, _P, _P,
+                                             _P]
+        L.fg8_gate_weights.restype = _I
+        L.fg8_gate_weights.argtypes = [_P, _P, _I64, _I, _I, _I64, _P, _P]
+        L.fg8_gate_backward.restype = _I
+        L.fg8_gate_backward.argtypes = [_P, _I, _I64, _P, _P, _P, _I64, _I, _I, _I, _P, _P, _P]
         L.fg8_route_topk.restype = _I
         L.fg8_route_topk.argtypes = [_P, _P, _I64, _I, _I, _P, _P, _P]
         L.fg8_unpermute_combine.restype = _I
@@ -224,6 +237,46 @@ def fg8_grouped_gemm_swiglu_quant(a, sa, b, sb, offsets, M_total, I, K, E, hq, s
            "fg8_grouped_gemm_swiglu_quant")
 
 
+def fg8_grouped_gemm_swiglu_quant_save(a, sa, b, sb, offsets, M_total, I, K, E, hq, sh, guq, sgu,
+                                       dev_status, stream=None):
+    _check(lib().fg8_grouped_gemm_swiglu_quant_save(_ptr(a), _ptr(sa), _ptr(b), _ptr(sb),
+                                                    _ptr(offsets), M_total, I, K, E, _ptr(hq),
+                                                    _ptr(sh), _ptr(guq), _ptr(sgu),
+                                                    _ptr(dev_status), _stream(stream)),
+           "fg8_grouped_gemm_swiglu_quant_save")
+
+
+def fg8_swiglu_backward_quant(dh, guq, sgu, row_w, offsets, R, I, E, dq, sd, dqT, sdT, hqT, shT,
+                              gate_dot, offsets_out, dev_status, stream=None):
+    _check(lib().fg8_swiglu_backward_quant(_ptr(dh), _ptr(guq), _ptr(sgu), _ptr(row_w),
+                                           _ptr(offsets), R, I, E, _ptr(dq), _ptr(sd), _ptr(dqT),
+                                           _ptr(sdT), _ptr(hqT), _ptr(shT), _ptr(gate_dot),
+                                           _ptr(offsets_out), _ptr(dev_status), _stream(stream)),
+           "fg8_swiglu_backward_quant")
+
+
+def fg8_requantize_colwise(xq, sx, T, K, row_token, offsets, R, E, xqT, saT, offsets_out,
+                           dev_status, stream=None):
+    _check(lib().fg8_requantize_colwise(_ptr(xq), _ptr(sx), T, K, _ptr(row_token), _ptr(offsets),
+                                        R, E, _ptr(xqT), _ptr(saT), _ptr(offsets_out),
+                                        _ptr(dev_status), _stream(stream)),
+           "fg8_requantize_colwise")
+
+
+def fg8_gate_weights(token_row, affinity, T, k, normalize, R, row_w, stream=None):
+    _check(lib().fg8_gate_weights(_ptr(token_row), _ptr(affinity), T, k, normalize, R,
+                                  _ptr(row_w), _stream(stream)),
+           "fg8_gate_weights")
+
+
+def fg8_gate_backward(gate_dot, nb, R, token_row, topk_ids, affinity, T, k, E, normalize,
+                      daffinity, dlogits, stream=None):
+    _check(lib().fg8_gate_backward(_ptr(gate_dot), nb, R, _ptr(token_row), _ptr(topk_ids),
+                                   _ptr(affinity), T, k, E, normalize, _ptr(daffinity),
+                                   _ptr(dlogits), _stream(stream)),
+           "fg8_gate_backward")
+
+
 def fg8_route_topk(logits, bias, T, E, k, ids, affinity, stream=None):
     _check(lib().fg8_route_topk(_ptr(logits), _ptr(bias), T, E, k, _ptr(ids), _ptr(affinity),
                                 _stream(stream)),
@@ -290,6 +343,21 @@ def _u16(x: torch.Tensor) -> torch.Tensor:
     if x.dtype in (torch.int16, torch.uint16):
         return x
     raise TypeError("expected bf16 data")
+
+
+def _out(t, shape, dtype, device):
+    """The caller's output tensor, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"output of shape {tuple(t.shape)} {t.dtype}, expected {tuple(shape)} {dtype}")
+    return t
+
+
+def _want(what, t, shape, dtype):
+    """Check an input tensor that a helper derives no size from."""
+    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
+        raise ValueError(f"{what} of shape {tuple(t.shape)} {t.dtype}, expected {tuple(shape)} {dtype}")
 
 
 def new_status(device=None) -> torch.Tensor:
@@ -443,6 +511,103 @@ def grouped_gemm_swiglu_quant(a, sa, b, sb, offsets, dev_status=None, hq=None, s
     fg8_grouped_gemm_swiglu_quant(a, sa, b, sb, offsets, M_total, I, K, E, hq, sh, dev_status,
                                   stream)
     return hq, sh
+
+
+def grouped_gemm_swiglu_quant_save(a, sa, b, sb, offsets, hq=None, sh=None, guq=None, sgu=None,
+                                   dev_status=None, stream=None):
+    """As grouped_gemm_swiglu_quant, keeping the gate and up projections in 8 bits
+    for the backward: -> (hq [M, I] u8, sh [I/128, M], guq [M, 2I] u8, sgu [2I/128, M])."""
+    M_total, K = a.shape
+    E, I = offsets.numel() - 1, b.shape[1] // 2
+    dev = a.device
+    _want("a", a, (M_total, K), torch.uint8)
+    _want("sa", sa, (K // 128, M_total), torch.float32)
+    _want("b", b, (E, 2 * I, K), torch.uint8)
+    _want("sb", sb, (E, 2 * I // 128, K // 128), torch.float32)
+    _want("offsets", offsets, (E + 1,), torch.int32)
+    hq = _out(hq, (M_total, I), torch.uint8, dev)
+    sh = _out(sh, (I // 128, M_total), torch.float32, dev)
+    guq = _out(guq, (M_total, 2 * I), torch.uint8, dev)
+    sgu = _out(sgu, (2 * I // 128, M_total), torch.float32, dev)
+    fg8_grouped_gemm_swiglu_quant_save(a, sa, b, sb, offsets, M_total, I, K, E, hq, sh, guq, sgu,
+                                       dev_status, stream)
+    return hq, sh, guq, sgu
+
+
+def swiglu_backward_quant(dh, guq, sgu, offsets, row_w=None, dq=None, sd=None, dqT=None, sdT=None,
+                          hqT=None, shT=None, gate_dot=None, offsets_out=None, dev_status=None,
+                          stream=None):
+    """dh bf16 [R, I] (gradient of the activation's output), guq/sgu (the 8-bit
+    gate and up) -> dict of the [dG dU] operand by rows (dq, sd) and by columns
+    (dqT, sdT), the weighted activation by columns (hqT, shT), gate_dot
+    [I/128, R] and the padded offsets_out."""
+    R, I = dh.shape
+    E, dev = offsets.numel() - 1, dh.device
+    P = fg8_colwise_capacity(R, E)
+    u8, f32 = torch.uint8, torch.float32
+    _want("guq", guq, (R, 2 * I), u8)
+    _want("sgu", sgu, (2 * I // 128, R), f32)
+    _want("offsets", offsets, (E + 1,), torch.int32)
+    _want("row_w", row_w, (R,), f32)
+    o = dict(dq=_out(dq, (R, 2 * I), u8, dev), sd=_out(sd, (2 * I // 128, R), f32, dev),
+             dqT=_out(dqT, (2 * I, P), u8, dev), sdT=_out(sdT, (P // 128, 2 * I), f32, dev),
+             hqT=_out(hqT, (I, P), u8, dev), shT=_out(shT, (P // 128, I), f32, dev),
+             gate_dot=_out(gate_dot, (I // 128, R), f32, dev),
+             offsets_out=_out(offsets_out, (E + 1,), torch.int32, dev))
+    fg8_swiglu_backward_quant(_u16(dh), guq, sgu, row_w, offsets, R, I, E, o["dq"], o["sd"],
+                              o["dqT"], o["sdT"], o["hqT"], o["shT"], o["gate_dot"],
+                              o["offsets_out"], dev_status, stream)
+    return o
+
+
+def requantize_colwise(xq, sx, offsets, row_token=None, xqT=None, saT=None, offsets_out=None,
+                       dev_status=None, stream=None):
+    """xq u8 [T, K], sx [K/128, T] (rows kept in 8 bits) -> (xqT [K, P] u8,
+    saT [P/128, K], padded offsets): quantize_act_colwise from the checkpoint."""
+    T, K = xq.shape
+    R = T if row_token is None else row_token.numel()
+    E, dev = offsets.numel() - 1, xq.device
+    P = fg8_colwise_capacity(R, E)
+    _want("xq", xq, (T, K), torch.uint8)
+    _want("sx", sx, (K // 128, T), torch.float32)
+    _want("offsets", offsets, (E + 1,), torch.int32)
+    _want("row_token", row_token, (R,), torch.int32)
+    xqT = _out(xqT, (K, P), torch.uint8, dev)
+    saT = _out(saT, (P // 128, K), torch.float32, dev)
+    offsets_out = _out(offsets_out, (E + 1,), torch.int32, dev)
+    fg8_requantize_colwise(xq, sx, T, K, row_token, offsets, R, E, xqT, saT, offsets_out,
+                           dev_status, stream)
+    return xqT, saT, offsets_out
+
+
+def gate_weights(token_row, affinity, R, normalize=True, row_w=None, stream=None):
+    """token_row int32 [T*k], affinity fp32 [T, k] -> row_w fp32 [R]: the combine's
+    gate weight of every routed row (0 where no slot names the row)."""
+    T, k = affinity.shape
+    _want("token_row", token_row.reshape(-1), (T * k,), torch.int32)
+    _want("affinity", affinity, (T, k), torch.float32)
+    if row_w is None:
+        row_w = torch.zeros(R, dtype=torch.float32, device=affinity.device)
+    _want("row_w", row_w, (R,), torch.float32)
+    fg8_gate_weights(token_row, affinity, T, k, int(bool(normalize)), R, row_w, stream)
+    return row_w
+
+
+def gate_backward(gate_dot, token_row, topk_ids, affinity, E, normalize=True, daffinity=None,
+                  dlogits=None, stream=None):
+    """gate_dot fp32 [I/128, R] (swiglu_backward_quant) -> (daffinity [T, k],
+    dlogits [T, E]): the gradients of the chosen affinities and router logits."""
+    nb, R = gate_dot.shape
+    T, k = affinity.shape
+    _want("gate_dot", gate_dot, (nb, R), torch.float32)
+    _want("token_row", token_row.reshape(-1), (T * k,), torch.int32)
+    _want("topk_ids", topk_ids.reshape(-1), (T * k,), torch.int32)
+    _want("affinity", affinity, (T, k), torch.float32)
+    daffinity = _out(daffinity, (T, k), torch.float32, affinity.device)
+    dlogits = _out(dlogits, (T, E), torch.float32, affinity.device)
+    fg8_gate_backward(gate_dot, nb, R, token_row, topk_ids, affinity, T, k, E,
+                      int(bool(normalize)), daffinity, dlogits, stream)
+    return daffinity, dlogits
 
 
 def grouped_gemm_combine(a, sa, b, sb, offsets, row_token, token_row, affinity, normalize=True,

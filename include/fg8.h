@@ -18,7 +18,9 @@
  *     s = fp32(amax / 448)   (s = 1 when amax == 0),
  *     q = E4M3(fp32(x / s))  round to nearest, ties to even, saturating at
  *                            +-448, sign of zero kept.
- * s is the dequantization multiplier: x ~= q * s.  NaN/Inf inputs are outside
+ * s is the dequantization multiplier: x ~= q * s.  (The calls that quantize fp32
+ * values down the token axis or save them take s = 2^-149 where amax / 448 rounds
+ * to 0.)  NaN/Inf inputs are outside
  * the contract (their outputs are unspecified).
  *
  * Conventions for every call:
@@ -302,6 +304,114 @@ fg8_status fg8_grouped_gemm_swiglu_quant(const uint8_t* a, const float* sa,
                                          const int32_t* offsets, int64_t M_total, int I, int K,
                                          int E, uint8_t* hq, float* sh, int32_t* dev_status,
                                          fg8_stream_t stream);
+
+/*
+ * fg8_grouped_gemm_swiglu_quant_save -- fg8_grouped_gemm_swiglu_quant that also
+ * keeps what the activation's backward needs: the gate and up projections as
+ * E4M3 codes in 1x128 tiles (2 bytes per activation where bf16 takes 4), formed
+ * from the same fp32 accumulators in the epilogue.  ([DS] sec. 2.2 quantizes the
+ * activations around the FP8 GEMMs in 1x128 tiles; keeping them so for the
+ * backward is the reading taken here.)
+ *   a, sa, b, sb, offsets, M_total, I, K, E, hq, sh, dev_status
+ *            as for fg8_grouped_gemm_swiglu_quant (hq, sh are the same values)
+ *   guq      E4M3 [M_total][2I]: gate in columns [0, I), up in [I, 2I)
+ *   sgu      fp32 [2I/128][M_total]; rows outside [0, offsets[E]) of both are
+ *            not written.  guq 16-byte aligned.
+ */
+fg8_status fg8_grouped_gemm_swiglu_quant_save(const uint8_t* a, const float* sa,
+                                              const uint8_t* b, const float* sb,
+                                              const int32_t* offsets, int64_t M_total, int I, int K,
+                                              int E, uint8_t* hq, float* sh, uint8_t* guq,
+                                              float* sgu, int32_t* dev_status, fg8_stream_t stream);
+
+/*
+ * fg8_swiglu_backward_quant -- the gated activation's backward from the 8-bit
+ * checkpoint, with the three quantizations that the backward's GEMMs need, in
+ * one pass.  For every row r in [0, offsets[E]) and column i, with g and u the
+ * checkpoint's values, dh the gradient of the activation's output before the
+ * gate weight (the down-projection's dgrad of the token's output gradient), w
+ * the row's gate weight and d = w dh:
+ *     sig = 1 / (1 + exp(-g)),   h = g sig u
+ *     dU = d g sig,   dG = d u sig (1 + g (1 - sig))
+ *     gate_dot[c][r] = sum over the columns of block c of dh h
+ * so that, the layer's output being sum_j w_j Wd h_j, the sum of a row's
+ * gate_dot over c is dL/dw (fg8_gate_backward).  Arithmetic in fp32 (fast
+ * exponential and reciprocal, a few ulp); each tile's scale is fp32(amax / 448)
+ * and its codes E4M3 (RNE, saturating) of the value times fp32(1 / scale),
+ * i.e. of the quotient to within 2^-22.
+ *   dh       bf16 [R][I]
+ *   guq, sgu E4M3 [R][2I], fp32 [2I/128][R]   (..._swiglu_quant_save)
+ *   row_w    fp32 [R] (fg8_gate_weights), or NULL: w = 1
+ *   offsets  int32 [E+1] on the device: expert e owns rows [offsets[e], offsets[e+1])
+ *   dq, sd   E4M3 [R][2I] of [dG dU], fp32 [2I/128][R]: by rows, the up
+ *            projection's dgrad operand (fg8_grouped_gemm, FG8_GROUP_M)
+ *   dqT, sdT E4M3 [2I][P], fp32 [P/128][2I] of [dG dU], and
+ *   hqT, shT E4M3 [I][P],  fp32 [P/128][I]  of w h: down the token axis, in the
+ *            layout of fg8_quantize_act's FG8_COLWISE mode (every expert's rows
+ *            in tiles of 128, zero-padded), P = fg8_colwise_capacity(R, E): the
+ *            weight gradients' operands (FG8_GROUP_K)
+ *   gate_dot fp32 [I/128][R], or NULL
+ *   offsets_out int32 [E+1]: padded offsets, as FG8_COLWISE
+ *   Rows outside [0, offsets[E]) and columns past offsets_out[E] are not
+ *   written.  I % 128 == 0, E <= 1024; dh, guq, dq, dqT, hqT 16-byte aligned.
+ *   A timed-out internal wait writes FG8_ERR_TIMEOUT to *dev_status.
+ */
+fg8_status fg8_swiglu_backward_quant(const uint16_t* dh, const uint8_t* guq, const float* sgu,
+                                     const float* row_w, const int32_t* offsets, int64_t R, int I,
+                                     int E, uint8_t* dq, float* sd, uint8_t* dqT, float* sdT,
+                                     uint8_t* hqT, float* shT, float* gate_dot,
+                                     int32_t* offsets_out, int32_t* dev_status,
+                                     fg8_stream_t stream);
+
+/*
+ * fg8_requantize_colwise -- the weight gradient's operand from rows that were
+ * kept in 8 bits: fg8_quantize_act's FG8_COLWISE mode whose input is the E4M3
+ * rows and scales of its FG8_ROWWISE mode (identity rows, or any rows of that
+ * layout) instead of bf16, so that a layer's input can be kept in 8 bits until
+ * the backward.  A value is x = fp32(code * scale); then, per column and tile of
+ * 128 rows of one expert, s = fp32(amax / 448) and q = E4M3(fp32(x / s)).
+ *   xq, sx    E4M3 [T][K], fp32 [K/128][T]
+ *   row_token int32 [R]: logical row r is xq's row row_token[r]; or NULL: R = T
+ *             and logical row r is row r.  An entry outside [0, T) gives a row of
+ *             zeros and FG8_ERR_INVALID_ARG in *dev_status.
+ *   offsets   int32 [E+1] on the device, over the R logical rows
+ *   xqT, saT, offsets_out  as FG8_COLWISE, P = fg8_colwise_capacity(R, E)
+ *   K % 128 == 0, E <= 1024; xq, xqT 16-byte aligned.
+ */
+fg8_status fg8_requantize_colwise(const uint8_t* xq, const float* sx, int64_t T, int64_t K,
+                                  const int32_t* row_token, const int32_t* offsets, int64_t R,
+                                  int E, uint8_t* xqT, float* saT, int32_t* offsets_out,
+                                  int32_t* dev_status, fg8_stream_t stream);
+
+/*
+ * fg8_gate_weights -- every routed row's gate weight: row_w[token_row[t*k + j]]
+ * = w[t][j], with w exactly as in fg8_unpermute_combine (the kept affinities
+ * summed in fp32 in slot order, one IEEE division when normalize = 1).  Rows
+ * that no slot names are not written.
+ *   token_row int32 [T*k], affinity fp32 [T][k], row_w fp32 [R]; 1 <= k <= 16
+ */
+fg8_status fg8_gate_weights(const int32_t* token_row, const float* affinity, int64_t T, int k,
+                            int normalize, int64_t R, float* row_w, fg8_stream_t stream);
+
+/*
+ * fg8_gate_backward -- the gate's gradient ([DS] sec. 2.1: sigmoid affinities;
+ * the selection and its bias have none).  With D[t][j] = sum over c < nb of
+ * gate_dot[c][token_row[t*k + j]] = dL/dw[t][j] (in block order, fp32) and S the
+ * sum of the token's kept affinities a:
+ *     da[t][j] = normalize ? (D[t][j] - sum_i w[t][i] D[t][i]) / S : D[t][j]
+ *     dlogits[t][e] = sum over the slots with topk_ids[t][j] == e of
+ *                     da[t][j] * a[t][j] * (1 - a[t][j]), 0 for all other e
+ * A slot without a row (outside [0, R)) and, with normalize, a token with S = 0
+ * get da = 0.  Sums run in slot order: results do not vary between runs.
+ *   gate_dot fp32 [nb][R] (fg8_swiglu_backward_quant), token_row, topk_ids
+ *   int32 [T*k], affinity fp32 [T][k]; daffinity fp32 [T][k]
+ *   dlogits  fp32 [T][E], written in full, or NULL (topk_ids may then be NULL)
+ *   1 <= k <= 16.  Ids outside [0, E) add nothing.
+ */
+fg8_status fg8_gate_backward(const float* gate_dot, int nb, int64_t R, const int32_t* token_row,
+                             const int32_t* topk_ids, const float* affinity, int64_t T, int k,
+                             int E, int normalize, float* daffinity, float* dlogits,
+                             fg8_stream_t stream);
 
 /*
  * fg8_route_topk -- sigmoid-affinity top-K routing with a per-expert bias
