@@ -52,11 +52,13 @@
 #include <cuda.h>
 
 #include "fg8_common.cuh"
+#include "fg8_tcgen05.cuh"
 #include "fg8_tma.cuh"
 
 namespace {
 
 using namespace fg8::tma;
+using namespace fg8::tc;
 
 // 128 x 256 tiles: N = 256 is the widest single-CTA tcgen05.mma.  Narrower
 // tiles do not pay here: 128 x 128 tiles with four TMEM buffers ran at 0.6x the
@@ -92,10 +94,7 @@ struct Warps {
 constexpr int kMaxE = 1024;
 constexpr uint32_t kTmemCols = 512;                // two partial buffers of BN columns
 
-// tcgen05 instruction descriptor (kind::f8f6f4): D = f32 (bits 4-5 = 1),
-// A = B = E4M3 (format 0), both K-major, N >> 3 in bits 17-22, M >> 4 in 24-28.
-constexpr uint32_t kIdesc =
-    (1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+constexpr uint32_t kIdesc = idesc_e4m3(BM, BN);
 
 // row-grouped epilogue staging: per promotion warp 32 rows x 16 words (+4 padding)
 constexpr int kStageWords = 20;
@@ -191,38 +190,6 @@ struct GemmArgs {
 // ---------------------------------------------------------------------------
 // PTX wrappers
 // ---------------------------------------------------------------------------
-
-// K-major operand tile in shared memory, 128-byte rows, 128-byte swizzle:
-// 8-row atoms 1024 bytes apart (stride byte offset), descriptor version 1.
-FG8_DEV uint64_t smem_desc(uint32_t addr) {
-    uint64_t d = 0;
-    d |= (uint64_t)((addr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)1 << 16;                  // leading byte offset (unused with this swizzle)
-    d |= (uint64_t)(1024 >> 4) << 32;        // stride byte offset
-    d |= (uint64_t)1 << 46;                  // descriptor version
-    d |= (uint64_t)2 << 61;                  // SWIZZLE_128B
-    return d;
-}
-
-FG8_DEV void mma_e4m3(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n"
-        ".reg .pred p;\n"
-        "setp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
-        "}\n" ::"r"(tmem_d),
-        "l"(adesc), "l"(bdesc), "r"(kIdesc), "r"(accumulate)
-        : "memory");
-}
-
-FG8_DEV void mma_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                     bar)
-                 : "memory");
-}
-
-FG8_DEV void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-FG8_DEV void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
 // out[0..3] += (x, y, z, w), one 16-byte fp32 reduction in L2 (16-byte aligned)
 FG8_DEV void red_add_v4(float* out, float x, float y, float z, float w) {
@@ -625,7 +592,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
 #pragma unroll
                     for (int kk = 0; kk < BK / 32; ++kk)
                         mma_e4m3(d, smem_desc(sA + 32 * kk), smem_desc(sA + kABytes + 32 * kk),
-                                 kk > 0 ? 1u : 0u);
+                                 kIdesc, kk > 0 ? 1u : 0u);
                     mma_commit(empty_bar(stage));
                     mma_commit(tfull_bar(buf));
                     if (++stage == kStages) {

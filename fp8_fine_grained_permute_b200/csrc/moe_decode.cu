@@ -1,0 +1,829 @@
+// moe_decode.cu -- the whole expert layer for a few tokens in one kernel.
+//
+// The layer as the chain of routing, permute + 1x128 quantize, gated
+// up-projection + 1x128 quantize, down-projection and combine computes it
+// (DeepSeek-V3 summary sec. 2.1, 2.2), for T <= 64 tokens:
+//     ids, a = top-k of sigmoid(logits) + bias;  w = a / sum a
+//     [G; U](p) = Wup[e] xq(t),  h(p) = quant(silu(G) U),  out(t) = sum_j w_j Wdn[e_j] h(t, j)
+// A few tokens read every weight of the experts they meet once and do next to no
+// arithmetic on it, so the time is that of 3 I C bytes an expert met over the HBM
+// rate, and what a kernel can lose is latency: launches, half-empty waves of tiles,
+// and pauses of the weight stream.  Hence
+//   * one cooperative launch, one CTA an SM.  The work of each of the two
+//     projections is a sequence of equal steps of 32 KB of weights, and every CTA
+//     takes an equal contiguous share of it, wherever that begins or ends
+//     (stream-K), so all SMs stream to the end for any number of experts.
+//   * weights are operand A of the tensor core (128 weight rows = M), tokens are
+//     operand B (N = 16 or 32 columns), so a token costs 128 bytes a step next to
+//     the weights' 32 KB instead of padding to a 128-row tile.  TMA brings the
+//     weights as they lie (E4M3, 128-byte swizzle) and the MMA reads them in
+//     shared memory: no thread touches a weight.
+//   * the weight producer runs ahead over the border between the projections: the
+//     ring is full of down-projection weights while the CTAs meet at the barrier.
+//
+// Step of the up-projection: one K block of a gate block and the matching up block
+// (2 x 128 x 128 bytes) for one group of at most N tokens of one expert.  Step of
+// the down-projection: two K blocks of 128 output columns.  A unit is what ends in
+// one result: (group, 128 columns of h), then 128 columns of out over all experts.
+// A unit cut between CTAs is joined from fp32 partials in the caller's workspace,
+// always in CTA order, so results do not vary between runs: for h the last CTA
+// to arrive joins (it needs the column maxima); for out, whose partials hold all
+// T tokens, every CTA that has a part joins its share of the rows.
+//
+// Warps: 0 TMA producer, 1 MMA issuer, 4..7 promotion (thread = one weight row:
+// acc[token] += partial * (activation scale * block scale), fp32), 8..11 fill
+// operand B: half a warp quantizes a token's 128 values of x (the bits of
+// fg8_quantize_act), or copies 128 codes of h.
+//
+// Every wait is bounded (FG8_ERR_TIMEOUT in *status; the roles wind down and TMEM
+// is released).
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include <type_traits>
+
+#include "fg8_columns.cuh"
+#include "fg8_route.cuh"
+#include "fg8_tcgen05.cuh"
+#include "fg8_tma.cuh"
+
+namespace {
+
+using namespace fg8::tma;
+using namespace fg8::tc;
+
+constexpr int kThreads = 384;
+constexpr int kMaxT = 64;
+constexpr int kMaxE = 1024;
+constexpr int kMaxCtas = 160;
+constexpr unsigned kFull = 0xffffffffu;
+constexpr uint32_t kABytes = 2 * 128 * 128;          // a step's weights
+constexpr int kTmemBufs = 4;
+constexpr int kFillWarps = 4;
+
+// Variants: N tokens a group.  N = 16 when T <= 16 (an expert then rarely has
+// more tokens and the ring is a stage deeper), else 32.
+template <int N>
+struct Cfg {
+    static constexpr int kStages = N == 16 ? 5 : 4;
+    static constexpr uint32_t kBBytes = 2 * N * 128;             // two K blocks of B (the first alone in the up-projection)
+    static constexpr uint32_t kStage = kABytes + kBBytes;
+    static constexpr int kTokens = N == 16 ? 16 : kMaxT;         // rows of the output accumulator
+    static constexpr int kPairs = kTokens * fg8::kRouteMaxK;
+    // factor slots: written for step n while steps up to n - kStages - kTmemBufs
+    // have been promoted (their stage and partial buffer were free again)
+    static constexpr int kSlots = kStages + kTmemBufs;
+    static constexpr uint32_t kTmemCols = kTmemBufs * 2 * N;     // 128 or 256
+    static constexpr uint32_t kOffAcc = kStages * kStage;        // float [kTokens][128]
+    static constexpr uint32_t kOffFactors = kOffAcc + kTokens * 512;
+    static constexpr uint32_t kOffRed = kOffFactors + kSlots * 2 * N * 4;   // float [2][4][N]
+    static constexpr uint32_t kOffBars = kOffRed + 2 * 4 * N * 4;
+    static constexpr int kNumBars = 2 * kStages + 2 * kTmemBufs + 1 + 1;    // full, empty, tfull, tempty, drain, group
+    static constexpr uint32_t kOffMisc = kOffBars + 8 * kNumBars;           // tmem slot, abort, generation, last[2]
+    static constexpr uint32_t kOffGroups = kOffMisc + 32;        // uint32 [kPairs]: n | first << 6 | expert << 16
+    static constexpr uint32_t kOffList = kOffGroups + 4 * kPairs;   // uint16 [kPairs]: pair, experts ascending
+    static constexpr uint32_t kOffW = kOffList + 2 * kPairs;     // float [kPairs]: gate weight of a pair
+    static constexpr uint32_t kOffIds = kOffW + 4 * kPairs;      // int32 [kPairs]
+    static constexpr uint32_t kOffCnt = kOffIds + 4 * kPairs;    // int32 [kMaxE + 1]
+    static constexpr uint32_t kOffWarp = kOffCnt + 4 * (kMaxE + 4);   // int32 [36]
+    static constexpr uint32_t kSmem = kOffWarp + 4 * 36 + 1024;  // + alignment slack
+    static_assert(kSmem <= 232448, "shared memory per CTA");
+    static_assert(kStage % 1024 == 0, "swizzle atoms");
+};
+
+// workspace: a fixed head of counters (zero between calls), then h, its scales
+// and the partials of cut units
+constexpr size_t kHeadBytes = FG8_MOE_DECODE_HEAD;
+struct Head {
+    uint32_t bar_count, bar_gen;
+    uint32_t pad[14];
+    uint32_t up_count[kMaxCtas];     // by the unit's first CTA
+    uint32_t down_count[kMaxCtas];   // by the unit's first CTA, cleared at the start of a call
+};
+static_assert(sizeof(Head) <= kHeadBytes, "counter head");
+
+struct Args {
+    const uint16_t* x;
+    const float* logits;
+    const float* bias;
+    int32_t* ids;
+    float* affinity;
+    const float* sw_up;      // [E][2 I / 128][C / 128]
+    const float* sw_dn;      // [E][C / 128][I / 128]
+    int T, k, E, C, I;
+    int normalize, out_f32;
+    void* out;
+    Head* head;
+    uint8_t* hq;             // [T k][I]
+    float* sh;               // [T k][I / 128]
+    float* part;             // [2 CTAs][part_floats]
+    int64_t part_floats;
+    int32_t* status;
+};
+
+FG8_DEV float silu_mul(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
+
+// 2 N consecutive TMEM columns of this thread's lane
+FG8_DEV void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,"
+        "%28,%29,%30,%31}, [%32];\n"
+        "tcgen05.wait::ld.sync.aligned;\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+          "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+          "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+          "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+
+// Contiguous shares of `total` equal steps: CTA c has [begin(c), begin(c + 1)).
+// No more CTAs take part than there are steps, so that every CTA from a unit's
+// first to its last has a part of it.
+struct Share {
+    int64_t total;
+    int ctas;
+    FG8_DEV Share(int64_t n, int all) : total(n), ctas((int)min(n, (int64_t)all)) {}
+    FG8_DEV int64_t begin(int c) const { return c >= ctas ? total : total * c / ctas; }
+    FG8_DEV int owner(int64_t step) const { return (int)(((step + 1) * ctas - 1) / total); }
+};
+
+template <int N>
+__global__ void __launch_bounds__(kThreads, 1)
+moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CUtensorMap tm_dn, const Args a) {
+    using K = Cfg<N>;
+    constexpr int S = K::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t bar0 = sbase + K::kOffBars;
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (S + s); };
+    auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * S + b); };
+    auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * S + kTmemBufs + b); };
+    const uint32_t drain_bar = bar0 + 8u * (2 * S + 2 * kTmemBufs);
+    const uint32_t group_bar = drain_bar + 8u;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + K::kOffMisc);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + K::kOffMisc + 4);
+    volatile uint32_t* s_gen = reinterpret_cast<volatile uint32_t*>(smem + K::kOffMisc + 8);
+    volatile int* s_last = reinterpret_cast<volatile int*>(smem + K::kOffMisc + 16);   // [2]
+    uint32_t* s_groups = reinterpret_cast<uint32_t*>(smem + K::kOffGroups);
+    uint16_t* s_list = reinterpret_cast<uint16_t*>(smem + K::kOffList);
+    float* s_w = reinterpret_cast<float*>(smem + K::kOffW);
+    int32_t* s_ids = reinterpret_cast<int32_t*>(smem + K::kOffIds);
+    int32_t* s_cnt = reinterpret_cast<int32_t*>(smem + K::kOffCnt);
+    float* s_factors = reinterpret_cast<float*>(smem + K::kOffFactors);
+    float* s_acc = reinterpret_cast<float*>(smem + K::kOffAcc);
+    float* s_red = reinterpret_cast<float*>(smem + K::kOffRed);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int cta = blockIdx.x, ctas = gridDim.x;
+    const int CB = a.C / 128, IB = a.I / 128, IB2 = (IB + 1) / 2;
+    const int R = a.T * a.k;
+
+    // ------------------------------------------------------------ set-up
+    if (tid == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full_bar(s), 2);      // weight producer (with the bytes), fill warp
+            mbar_init(empty_bar(s), 1);
+        }
+        for (int b = 0; b < kTmemBufs; ++b) {
+            mbar_init(tfull_bar(b), 1);
+            mbar_init(tempty_bar(b), 4);
+        }
+        mbar_init(drain_bar, 1);
+        mbar_init(group_bar, 4);
+        *abort_flag = 0;
+        // before this CTA arrives at the grid barrier its generation cannot change
+        *s_gen = fg8::ld_acquire_gpu(&a.head->bar_gen);
+        a.head->down_count[cta] = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(K::kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    for (int e = tid; e <= a.E; e += kThreads) s_cnt[e] = 0;
+
+    // ------------------------------------------------------------ routing
+    // every CTA routes every token: cheaper than a second grid barrier
+    float* s_aff = s_w;   // turned into weights below
+    if (a.logits) {
+        auto route = [&](auto per_lane) {
+            constexpr int PL = decltype(per_lane)::value;
+            float bl[PL];
+#pragma unroll
+            for (int i = 0; i < PL; ++i) bl[i] = lane + 32 * i < a.E ? a.bias[lane + 32 * i] : 0.f;
+            for (int t = warp; t < a.T; t += kThreads / 32) {
+                int32_t id;
+                float s;
+                fg8::route_token<PL>(a.logits + (int64_t)t * a.E, bl, a.E, a.k, lane, id, s);
+                if (lane < a.k) {
+                    s_ids[t * a.k + lane] = id;
+                    s_aff[t * a.k + lane] = s;
+                    if (cta == 0) {
+                        a.ids[t * a.k + lane] = id;
+                        a.affinity[t * a.k + lane] = s;
+                    }
+                }
+            }
+        };
+        if (a.E <= 64) route(std::integral_constant<int, 2>());
+        else if (a.E <= 256) route(std::integral_constant<int, 8>());
+        else route(std::integral_constant<int, 32>());
+    } else {
+        for (int p = tid; p < R; p += kThreads) {
+            int32_t id = a.ids[p];
+            if (id < 0 || id >= a.E) {
+                fg8::set_status(a.status, FG8_ERR_BAD_EXPERT_ID);
+                id = -1;
+            }
+            s_ids[p] = id;
+            s_aff[p] = a.affinity[p];
+        }
+    }
+    __syncthreads();
+    // a pair's place among its expert's pairs, in pair order: every CTA has to get
+    // the same lists (they index the partials that CTAs join), so one warp counts
+    if (warp == 0) {
+        for (int p0 = 0; p0 < R; p0 += 32) {
+            const int p = p0 + lane, id = p < R ? s_ids[p] : -1;
+            const unsigned same = __match_any_sync(kFull, id);
+            const int before = id >= 0 ? s_cnt[id] : 0;
+            __syncwarp();
+            if (id >= 0) {
+                const int rank = __popc(same & ((1u << lane) - 1u));
+                s_ids[p] = id | ((before + rank) << 10);
+                if (rank == 0) s_cnt[id] = before + __popc(same);
+            }
+            __syncwarp();
+        }
+    }
+    __syncthreads();
+    // one thread a token: its gate weights, as fg8_unpermute_combine
+    if (a.normalize && tid < a.T) {
+        float sum = 0.f;
+        for (int j = 0; j < a.k; ++j)
+            if (s_ids[tid * a.k + j] >= 0) sum = __fadd_rn(sum, s_aff[tid * a.k + j]);
+        for (int j = 0; j < a.k; ++j)
+            s_w[tid * a.k + j] = sum != 0.f ? __fdiv_rn(s_aff[tid * a.k + j], sum) : 0.f;
+    }
+    // exclusive prefix of pairs (low half) and of groups (high half) over experts
+    for (int e = tid; e < a.E; e += kThreads) {
+        const int c = s_cnt[e];
+        s_cnt[e] = c | ((c + N - 1) / N << 16);
+    }
+    __syncthreads();
+    fg8::block_exclusive_scan(s_cnt, s_cnt, a.E, reinterpret_cast<int32_t*>(smem + K::kOffWarp));
+    for (int p = tid; p < R; p += kThreads) {
+        const int v = s_ids[p];
+        if (v >= 0) s_list[(s_cnt[v & 1023] & 0xFFFF) + (v >> 10)] = (uint16_t)p;
+    }
+    for (int e = tid; e < a.E; e += kThreads) {
+        const int lo = s_cnt[e], hi = s_cnt[e + 1];
+        int first = lo & 0xFFFF;
+        const int end = hi & 0xFFFF;
+        for (int g = lo >> 16; g < (hi >> 16); ++g, first += N)
+            s_groups[g] = (uint32_t)min(N, end - first) | ((uint32_t)first << 6) | ((uint32_t)e << 16);
+    }
+    const int G = s_cnt[a.E] >> 16;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+
+    const Share up((int64_t)G * IB * CB, ctas), dn((int64_t)CB * G * IB2, ctas);
+    const int64_t u0 = up.begin(cta), u1 = up.begin(cta + 1);
+    const int64_t d0 = dn.begin(cta), d1 = dn.begin(cta + 1);
+    const int64_t unit_dn = (int64_t)G * IB2;    // steps of an output block
+    auto group_n = [&](uint32_t g) { return (int)(g & 63u); };
+    auto group_first = [&](uint32_t g) { return (int)((g >> 6) & 1023u); };
+    auto group_e = [&](uint32_t g) { return (int)(g >> 16); };
+
+    bool ok = true;
+    if (warp == 0) {
+        if (lane == 0) {
+            // -------------------------------------------- weight producer
+            uint32_t stage = 0, phase = 0;
+            auto take = [&]() { return mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, a.status); };
+            auto next = [&]() {
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            };
+            if (u0 < u1) {
+                int cb = (int)(u0 % CB), u = (int)(u0 / CB);
+                int ib = u % IB, g = u / IB;
+                for (int64_t s = u0; s < u1; ++s) {
+                    if (!(ok = take())) break;
+                    const uint32_t dst = sbase + stage * K::kStage;
+                    const int row = group_e(s_groups[g]) * 2 * a.I + 128 * ib;
+                    mbar_arrive_expect_tx(full_bar(stage), kABytes);
+                    tma_load_2d(&tm_up, dst, full_bar(stage), 128 * cb, row);
+                    tma_load_2d(&tm_up, dst + kABytes / 2, full_bar(stage), 128 * cb, row + a.I);
+                    next();
+                    if (++cb == CB) {
+                        cb = 0;
+                        if (++ib == IB) ib = 0, ++g;
+                    }
+                }
+            }
+            if (ok && d0 < d1) {
+                int cb = (int)(d0 / unit_dn), r = (int)(d0 % unit_dn);
+                int g = r / IB2, k2 = r % IB2;
+                for (int64_t s = d0; s < d1; ++s) {
+                    if (!(ok = take())) break;
+                    const uint32_t dst = sbase + stage * K::kStage;
+                    const int row = group_e(s_groups[g]) * a.C + 128 * cb;
+                    const bool two = 2 * k2 + 1 < IB;
+                    mbar_arrive_expect_tx(full_bar(stage), two ? kABytes : kABytes / 2);
+                    tma_load_2d(&tm_dn, dst, full_bar(stage), 256 * k2, row);
+                    if (two) tma_load_2d(&tm_dn, dst + kABytes / 2, full_bar(stage), 256 * k2 + 128, row);
+                    next();
+                    if (++k2 == IB2) {
+                        k2 = 0;
+                        if (++g == G) g = 0, ++cb;
+                    }
+                }
+            }
+            if (!ok) {   // let copies already issued land before the CTA winds down
+                const uint32_t last = (stage + S - 1) % S, lp = stage == 0 ? (phase ^ 1u) : phase;
+                const uint64_t t0 = fg8::globaltimer_ns();
+                while (!mbar_try_wait(full_bar(last), lp) && fg8::globaltimer_ns() - t0 < 100000000ull) {
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // -------------------------------------------- MMA issuer
+            constexpr uint32_t kIdesc = idesc_e4m3(128, N);
+            uint32_t stage = 0, phase = 0, buf = 0, bphase = 0;
+            int k2 = d0 < d1 ? (int)(d0 % unit_dn) % IB2 : 0;
+            const int64_t n_up = u1 - u0, n_all = n_up + (d1 - d0);
+            for (int64_t n = 0; n < n_all; ++n) {
+                if (!mbar_wait(tempty_bar(buf), bphase ^ 1u, abort_flag, a.status) ||
+                    !mbar_wait(full_bar(stage), phase, abort_flag, a.status))
+                    break;
+                tc_fence_after();
+                const uint32_t sA = sbase + stage * K::kStage, sB = sA + kABytes;
+                const uint32_t d = tmem_base + buf * 2 * N;
+                const bool is_up = n < n_up;
+                const bool two = is_up || 2 * k2 + 1 < IB;
+                const uint32_t sB2 = is_up ? sB : sB + N * 128;
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_e4m3(d, smem_desc(sA + 32 * kk), smem_desc(sB + 32 * kk), kIdesc, kk > 0 ? 1u : 0u);
+                if (two) {
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_e4m3(d + N, smem_desc(sA + kABytes / 2 + 32 * kk), smem_desc(sB2 + 32 * kk), kIdesc,
+                                 kk > 0 ? 1u : 0u);
+                }
+                mma_commit(empty_bar(stage));
+                mma_commit(tfull_bar(buf));
+                if (!is_up && ++k2 == IB2) k2 = 0;
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+                if (++buf == kTmemBufs) {
+                    buf = 0;
+                    bphase ^= 1u;
+                }
+            }
+            // all MMAs issued by this thread are complete once drain_bar flips
+            mma_commit(drain_bar);
+            const uint64_t t0 = fg8::globaltimer_ns();
+            while (!mbar_try_wait(drain_bar, 0) && fg8::globaltimer_ns() - t0 < 100000000ull) {
+            }
+        }
+    } else if (warp >= 8) {
+        // ------------------------------------------------ operand B
+        const int fw = warp - 8;
+        const int half = lane >> 4, hl = lane & 15;
+        const int64_t n_up = u1 - u0, n_all = n_up + (d1 - d0);
+        bool passed = false;   // the grid barrier
+        for (int64_t n = fw; n < n_all; n += kFillWarps) {
+            const uint32_t stage = (uint32_t)(n % S), phase = (uint32_t)(n / S) & 1u;
+            float* f = s_factors + (int)(n % K::kSlots) * 2 * N;
+            uint8_t* B = smem + stage * K::kStage + kABytes;
+            if (n < n_up) {
+                const int64_t s = u0 + n;
+                const int cb = (int)(s % CB), u = (int)(s / CB), ib = u % IB;
+                const uint32_t g = s_groups[u / IB];
+                const int cnt = group_n(g), first = group_first(g);
+                const float* sw = a.sw_up + ((int64_t)group_e(g) * 2 * IB + ib) * CB + cb;
+                const float swg = __ldg(sw), swu = __ldg(sw + (int64_t)IB * CB);
+                uint4 v[N / 2];   // this half-warp's tokens, 8 values a lane
+#pragma unroll
+                for (int i = 0; i < N / 2; ++i) {
+                    const int j = 2 * i + half;
+                    v[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (j < cnt)
+                        v[i] = __ldg(reinterpret_cast<const uint4*>(a.x + (int64_t)(s_list[first + j] / a.k) * a.C +
+                                                                    128 * cb + 8 * hl));
+                }
+                if (!(ok = mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, a.status))) break;
+#pragma unroll
+                for (int i = 0; i < N / 2; ++i) {
+                    if (2 * i < cnt) {   // warp-uniform
+                        const int j = 2 * i + half;
+                        float m = fg8::amax8(v[i]);
+#pragma unroll
+                        for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+                        const float sc = fg8::tile_scale(m);
+                        const uint2 q = fg8::quant8(v[i], fg8::make_qscale(sc));
+                        *reinterpret_cast<uint2*>(B + j * 128 + (((hl >> 1) ^ (j & 7)) << 4) + 8 * (hl & 1)) = q;
+                        if (hl == 0) {
+                            f[j] = sc * swg;
+                            f[N + j] = sc * swu;
+                        }
+                    }
+                }
+            } else {
+                if (!passed) {
+                    // all of h is written once every CTA has arrived
+                    if (lane == 0) {
+                        const uint64_t t0 = fg8::globaltimer_ns();
+                        while (fg8::ld_acquire_gpu(&a.head->bar_gen) == *s_gen) {
+                            if (*abort_flag) break;
+                            if (fg8::globaltimer_ns() - t0 > fg8::kWaitLimitNs) {
+                                fg8::set_status(a.status, FG8_ERR_TIMEOUT);
+                                *abort_flag = 1;
+                                break;
+                            }
+                        }
+                        __threadfence();
+                    }
+                    __syncwarp();
+                    if (*abort_flag) {
+                        ok = false;
+                        break;
+                    }
+                    passed = true;
+                }
+                const int64_t s = d0 + (n - n_up);
+                const int cb = (int)(s / unit_dn), r = (int)(s % unit_dn), k2 = r % IB2;
+                const uint32_t g = s_groups[r / IB2];
+                const int cnt = group_n(g), first = group_first(g);
+                const bool mine = 2 * k2 + (hl >> 3) < IB;   // this lane's K block exists
+                uint4 v[N / 2];
+#pragma unroll
+                for (int i = 0; i < N / 2; ++i) {
+                    const int j = 2 * i + half;
+                    v[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (j < cnt && mine)
+                        v[i] = __ldcg(reinterpret_cast<const uint4*>(a.hq + (int64_t)s_list[first + j] * a.I +
+                                                                     256 * k2 + 16 * hl));
+                }
+                // factors: lane = token of the first block, then of the second
+                float fac[2 * N / 32];
+#pragma unroll
+                for (int i = 0; i < 2 * N / 32; ++i) {
+                    const int idx = 32 * i + lane, j = idx % N, kb = 2 * k2 + idx / N;
+                    fac[i] = 0.f;
+                    if (j < cnt && kb < IB) {
+                        const int p = s_list[first + j];
+                        fac[i] = __ldcg(a.sh + (int64_t)p * IB + kb) *
+                                 __ldg(a.sw_dn + ((int64_t)group_e(g) * CB + cb) * IB + kb) * s_w[p];
+                    }
+                }
+                if (!(ok = mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, a.status))) break;
+#pragma unroll
+                for (int i = 0; i < N / 2; ++i) {
+                    const int j = 2 * i + half;
+                    if (j < cnt)
+                        *reinterpret_cast<uint4*>(B + (hl >> 3) * N * 128 + j * 128 + (((hl & 7) ^ (j & 7)) << 4)) = v[i];
+                }
+#pragma unroll
+                for (int i = 0; i < 2 * N / 32; ++i) f[32 * i + lane] = fac[i];
+            }
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full_bar(stage));
+        }
+    } else if (warp >= 4) {
+        // ------------------------------------------------ promotion
+        const int quarter = warp & 3;
+        const int row = 32 * quarter + lane;     // weight row of the tile
+        const uint32_t lane_base = tmem_base + ((uint32_t)(32 * quarter) << 16);
+        uint32_t buf = 0, bphase = 0, gphase = 0, joint = 0;
+        int slot = 0;
+        // barrier of the four promotion warps (bounded: false after an abort)
+        auto meet = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(group_bar);
+            const bool r = mbar_wait(group_bar, gphase, abort_flag, a.status);
+            gphase ^= 1u;
+            return __all_sync(kFull, r) != 0;
+        };
+        float acc[2 * N];
+        // acc[i] += partial[i] * factor[i] for one step's 2 N columns (the first
+        // half only where the step has one K block)
+        auto promote = [&](bool two) {
+            if (!__all_sync(kFull, mbar_wait(tfull_bar(buf), bphase, abort_flag, a.status))) return false;
+            tc_fence_after();
+            const float4* f4 = reinterpret_cast<const float4*>(s_factors + slot * 2 * N);
+#pragma unroll
+            for (int h = 0; h < 2 * N / 32; ++h) {
+                uint32_t p[32];
+                tmem_ld(lane_base + buf * 2 * N + 32 * h, p);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const int i = 32 * h + 4 * q;
+                    if (i >= N && !two) continue;
+                    const float4 f = f4[8 * h + q];
+                    acc[i] = fmaf(__uint_as_float(p[4 * q]), f.x, acc[i]);
+                    acc[i + 1] = fmaf(__uint_as_float(p[4 * q + 1]), f.y, acc[i + 1]);
+                    acc[i + 2] = fmaf(__uint_as_float(p[4 * q + 2]), f.z, acc[i + 2]);
+                    acc[i + 3] = fmaf(__uint_as_float(p[4 * q + 3]), f.w, acc[i + 3]);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tempty_bar(buf));
+            if (++buf == kTmemBufs) {
+                buf = 0;
+                bphase ^= 1u;
+            }
+            if (++slot == K::kSlots) slot = 0;
+            return true;
+        };
+        // where CTA c keeps its partial of a unit that begins at step `begin`
+        auto part_of = [&](int c, const Share& sh, int64_t begin) {
+            return a.part + (int64_t)(2 * c + (begin > sh.begin(c) ? 1 : 0)) * a.part_floats;
+        };
+
+        // ---- up-projection
+        if (u0 < u1) {
+            int cb = (int)(u0 % CB), u = (int)(u0 / CB);
+#pragma unroll
+            for (int i = 0; i < 2 * N; ++i) acc[i] = 0.f;
+            for (int64_t s = u0; ok && s < u1; ++s) {
+                if (!(ok = promote(true))) break;
+                if (++cb < CB && s + 1 < u1) continue;
+                // this CTA's part of unit u is done
+                const int ib = u % IB;
+                const uint32_t g = s_groups[u / IB];
+                const int cnt = group_n(g), first = group_first(g);
+                const int64_t ub = (int64_t)u * CB, ue = ub + CB;
+                bool finish = true;
+                if (ub < u0 || ue > u1) {
+                    float* my = part_of(cta, up, ub) + row;
+#pragma unroll
+                    for (int j = 0; j < N; ++j)
+                        if (j < cnt) {
+                            __stcg(my + j * 128, acc[j]);
+                            __stcg(my + (N + j) * 128, acc[N + j]);
+                        }
+                    __threadfence();
+                    if (!(ok = meet())) break;
+                    const int c0 = up.owner(ub), c1 = up.owner(ue - 1);
+                    if (warp == 4 && lane == 0) {
+                        __threadfence();
+                        const uint32_t limit = (uint32_t)(c1 - c0);
+                        const uint32_t old = atomicInc(&a.head->up_count[c0], limit);   // back to 0 after the last
+                        if (old > limit) fg8::set_status(a.status, FG8_ERR_WORKSPACE_SHARED);
+                        s_last[joint & 1u] = old >= limit;
+                    }
+                    if (!(ok = meet())) break;
+                    finish = s_last[joint & 1u] != 0;
+                    if (finish) {
+                        __threadfence();
+#pragma unroll
+                        for (int i = 0; i < 2 * N; ++i) acc[i] = 0.f;
+                        for (int c = c0; c <= c1; ++c) {
+                            const float* pp = part_of(c, up, ub) + row;
+#pragma unroll
+                            for (int j = 0; j < N; ++j)
+                                if (j < cnt) {
+                                    acc[j] += __ldcg(pp + j * 128);
+                                    acc[N + j] += __ldcg(pp + (N + j) * 128);
+                                }
+                        }
+                    }
+                }
+                if (finish) {
+                    // h = silu(gate) up for this row's column of every token, one
+                    // 1x128 tile a token over the 128 threads
+                    float* red = s_red + (joint & 1u) * 4 * N;
+#pragma unroll
+                    for (int j = 0; j < N; ++j)
+                        if (j < cnt) {
+                            acc[j] = silu_mul(acc[j], acc[N + j]);
+                            const uint32_t m = __reduce_max_sync(kFull, __float_as_uint(fabsf(acc[j])));
+                            if (lane == 0) red[quarter * N + j] = __uint_as_float(m);
+                        }
+                    if (!(ok = meet())) break;
+#pragma unroll
+                    for (int j = 0; j < N; ++j)
+                        if (j < cnt) {
+                            const float m = fmaxf(fmaxf(red[j], red[N + j]), fmaxf(red[2 * N + j], red[3 * N + j]));
+                            const float sc = fg8::tile_scale32(m);
+                            const int p = s_list[first + j];
+                            a.hq[(int64_t)p * a.I + 128 * ib + row] =
+                                (uint8_t)fg8::cvt_e4m3x2(__fdiv_rn(acc[j], sc), 0.f);
+                            if (row == 0) a.sh[(int64_t)p * IB + ib] = sc;
+                        }
+                }
+                ++joint;
+                cb = 0;
+                ++u;
+#pragma unroll
+                for (int i = 0; i < 2 * N; ++i) acc[i] = 0.f;
+            }
+        }
+        // ---- grid barrier: this CTA's h is written
+        if (ok) {
+            __threadfence();
+            if ((ok = meet()) && warp == 4 && lane == 0) {
+                __threadfence();
+                const uint32_t old = atomicInc(&a.head->bar_count, (uint32_t)ctas - 1u);
+                if (old > (uint32_t)ctas - 1u) fg8::set_status(a.status, FG8_ERR_WORKSPACE_SHARED);
+                if (old == (uint32_t)ctas - 1u) {
+                    __threadfence();
+                    atomicAdd(&a.head->bar_gen, 1u);
+                }
+            }
+        }
+        // ---- down-projection
+        auto store_out = [&](int t, int c, float v) {
+            if (a.out_f32) static_cast<float*>(a.out)[(int64_t)t * a.C + c] = v;
+            else static_cast<uint16_t*>(a.out)[(int64_t)t * a.C + c] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+        };
+        if (ok && d0 < d1) {
+            int cb = (int)(d0 / unit_dn), r = (int)(d0 % unit_dn);
+            int g = r / IB2, k2 = r % IB2;
+            for (int t = 0; t < a.T; ++t) s_acc[t * 128 + row] = 0.f;   // this thread's column, its alone
+#pragma unroll
+            for (int i = 0; i < 2 * N; ++i) acc[i] = 0.f;
+            for (int64_t s = d0; ok && s < d1; ++s) {
+                if (!(ok = promote(2 * k2 + 1 < IB))) break;
+                const bool cut = s + 1 == d1;
+                if (++k2 < IB2 && !cut) continue;
+                k2 = 0;
+                // the group's (or this CTA's last) columns into their tokens' sums
+                const uint32_t gr = s_groups[g];
+                const int cnt = group_n(gr), first = group_first(gr);
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    if (j < cnt) {
+                        float* o = s_acc + (s_list[first + j] / a.k) * 128 + row;
+                        *o += acc[j] + acc[N + j];
+                    }
+#pragma unroll
+                for (int i = 0; i < 2 * N; ++i) acc[i] = 0.f;
+                if (++g < G && !cut) continue;
+                g = 0;
+                // this CTA's part of output block cb is done
+                const int64_t ub = (int64_t)cb * unit_dn, ue = ub + unit_dn;
+                if (ub >= d0 && ue <= d1) {
+                    for (int t = 0; t < a.T; ++t) store_out(t, 128 * cb + row, s_acc[t * 128 + row]);
+                } else {
+                    float* my = part_of(cta, dn, ub) + row;
+                    for (int t = 0; t < a.T; ++t) __stcg(my + t * 128, s_acc[t * 128 + row]);
+                    __threadfence();
+                    if (!(ok = meet())) break;
+                    if (warp == 4 && lane == 0) {
+                        __threadfence();
+                        atomicAdd(&a.head->down_count[dn.owner(ub)], 1u);
+                    }
+                }
+                for (int t = 0; t < a.T; ++t) s_acc[t * 128 + row] = 0.f;
+                ++cb;
+            }
+            // cut blocks (at most the first and the last of this CTA's): once all
+            // their parts are there, each of their CTAs joins its share of the tokens
+            const int cb0 = (int)(d0 / unit_dn), cb1 = (int)((d1 - 1) / unit_dn);
+            for (int w = 0; ok && w < 2; ++w) {
+                const int c = w == 0 ? cb0 : cb1;
+                if (w == 1 && cb1 == cb0) break;
+                const int64_t ub = (int64_t)c * unit_dn, ue = ub + unit_dn;
+                if (ub >= d0 && ue <= d1) continue;
+                const int c0 = dn.owner(ub), c1 = dn.owner(ue - 1), n = c1 - c0 + 1;
+                if (warp == 4 && lane == 0) {
+                    const uint64_t t0 = fg8::globaltimer_ns();
+                    while (fg8::ld_acquire_gpu(&a.head->down_count[c0]) < (uint32_t)n) {
+                        if (*abort_flag) break;
+                        if (fg8::globaltimer_ns() - t0 > fg8::kWaitLimitNs) {
+                            fg8::set_status(a.status, FG8_ERR_TIMEOUT);
+                            *abort_flag = 1;
+                            break;
+                        }
+                    }
+                    __threadfence();
+                }
+                if (!(ok = meet()) || *abort_flag) break;
+                const int t1 = a.T * (cta - c0 + 1) / n;
+                for (int t = a.T * (cta - c0) / n; t < t1; ++t) {
+                    float v = 0.f;
+                    for (int q = c0; q <= c1; ++q) v += __ldcg(part_of(q, dn, ub) + t * 128 + row);
+                    store_out(t, 128 * c + row, v);
+                }
+            }
+        }
+        // no pair has an expert: the output is zero
+        if (G == 0)
+            for (int c = cta; c < CB; c += ctas)
+                for (int t = 0; t < a.T; ++t) store_out(t, 128 * c + row, 0.f);
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(K::kTmemCols)
+                     : "memory");
+    }
+}
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+struct Layout {
+    size_t hq, sh, part, total;
+    int64_t part_floats;
+};
+Layout layout(int64_t T, int k, int64_t I) {
+    Layout l;
+    const int64_t R = T * k;
+    l.part_floats = 128 * (T > 64 ? T : 64);   // 2 N columns of a group, or T tokens
+    l.hq = kHeadBytes;
+    l.sh = l.hq + round256((size_t)(R * I));
+    l.part = l.sh + round256((size_t)(R * (I / 128) * 4));
+    l.total = l.part + (size_t)(2 * kMaxCtas * l.part_floats * 4);
+    return l;
+}
+
+template <int N>
+fg8_status launch(const CUtensorMap& up, const CUtensorMap& dn, Args& a, cudaStream_t st) {
+    auto kern = moe_decode<N>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<N>::kSmem) != cudaSuccess)
+        return FG8_ERR_CUDA;
+    int grid = fg8h::num_sms();
+    if (grid > kMaxCtas) grid = kMaxCtas;
+    void* args[] = {const_cast<CUtensorMap*>(&up), const_cast<CUtensorMap*>(&dn), &a};
+    if (cudaLaunchCooperativeKernel((const void*)kern, dim3((unsigned)grid), dim3(kThreads), args, Cfg<N>::kSmem,
+                                    st) != cudaSuccess) {
+        cudaGetLastError();
+        return FG8_ERR_CUDA;
+    }
+    return FG8_OK;
+}
+
+}  // namespace
+
+extern "C" size_t fg8_moe_decode_workspace(int64_t T, int k, int64_t C, int64_t I) {
+    (void)C;
+    if (T < 1 || T > kMaxT || k < 1 || k > fg8::kRouteMaxK || I < 128) return 0;
+    return layout(T, k, I).total;
+}
+
+extern "C" fg8_status fg8_moe_decode(const uint16_t* x, int64_t T, int C, const float* logits, const float* bias,
+                                     int32_t* topk_ids, float* affinity, int k, int E, const uint8_t* wq_up,
+                                     const float* sw_up, int I, const uint8_t* wq_dn, const float* sw_dn,
+                                     int normalize, int out_dtype, void* out, void* workspace, size_t ws_bytes,
+                                     int32_t* dev_status, fg8_stream_t stream) {
+    if (T < 0 || C < 128 || C % 128 || I < 128 || I % 128 || E < 1 || k < 1 || k > E ||
+        (normalize != 0 && normalize != 1))
+        return FG8_ERR_INVALID_ARG;
+    if (out_dtype != FG8_OUT_BF16 && out_dtype != FG8_OUT_F32) return FG8_ERR_INVALID_ARG;
+    if (T > kMaxT || k > fg8::kRouteMaxK || E > kMaxE) return FG8_ERR_UNSUPPORTED;
+    if ((int64_t)E * 2 * I > INT32_MAX || (int64_t)E * C > INT32_MAX) return FG8_ERR_UNSUPPORTED;
+    if (T == 0) return FG8_OK;
+    if (!x || !topk_ids || !affinity || !wq_up || !sw_up || !wq_dn || !sw_dn || !out || !workspace ||
+        (logits && !bias))
+        return FG8_ERR_INVALID_ARG;
+    if (!fg8h::aligned16(x) || !fg8h::aligned16(wq_up) || !fg8h::aligned16(wq_dn) || !fg8h::aligned16(out) ||
+        !fg8h::aligned16(workspace) ||
+        ((reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(bias) |
+          reinterpret_cast<uintptr_t>(topk_ids) | reinterpret_cast<uintptr_t>(affinity) |
+          reinterpret_cast<uintptr_t>(sw_up) | reinterpret_cast<uintptr_t>(sw_dn)) & 3))
+        return FG8_ERR_INVALID_ARG;
+    const Layout l = layout(T, k, I);
+    if (ws_bytes < l.total) return FG8_ERR_INVALID_ARG;
+    CUtensorMap up, dn;
+    if (!fg8h::make_tensor_map_2d(&up, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, wq_up, (uint64_t)E * 2 * I, (uint64_t)C, 128,
+                                  128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !fg8h::make_tensor_map_2d(&dn, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, wq_dn, (uint64_t)E * C, (uint64_t)I, 128,
+                                  128, CU_TENSOR_MAP_SWIZZLE_128B))
+        return FG8_ERR_CUDA;
+    Args a;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    a.x = x; a.logits = logits; a.bias = bias; a.ids = topk_ids; a.affinity = affinity;
+    a.sw_up = sw_up; a.sw_dn = sw_dn;
+    a.T = (int)T; a.k = k; a.E = E; a.C = C; a.I = I;
+    a.normalize = normalize; a.out_f32 = out_dtype == FG8_OUT_F32; a.out = out;
+    a.head = reinterpret_cast<Head*>(ws);
+    a.hq = ws + l.hq;
+    a.sh = reinterpret_cast<float*>(ws + l.sh);
+    a.part = reinterpret_cast<float*>(ws + l.part);
+    a.part_floats = l.part_floats;
+    a.status = dev_status;
+    return T <= 16 ? launch<16>(up, dn, a, (cudaStream_t)stream) : launch<32>(up, dn, a, (cudaStream_t)stream);
+}

@@ -39,6 +39,7 @@ FG8_GROUP_M = 0
 FG8_GROUP_K = 1
 FG8_BSCALE_BLOCK128 = 0
 FG8_BSCALE_ROW128 = 1
+FG8_MOE_DECODE_HEAD = 4096
 
 
 class FG8Error(RuntimeError):
@@ -111,6 +112,11 @@ def lib() -> ctypes.CDLL:
         L.fg8_grouped_gemm_combine.restype = _I
         L.fg8_grouped_gemm_combine.argtypes = [_P, _P, _P, _P, _P, _I64, _I, _I, _I, _P, _P, _P,
                                                _I64, _I, _I, _P, _P, _SZ, _P, _P]
+        L.fg8_moe_decode_workspace.restype = _SZ
+        L.fg8_moe_decode_workspace.argtypes = [_I64, _I, _I64, _I64]
+        L.fg8_moe_decode.restype = _I
+        L.fg8_moe_decode.argtypes = [_P, _I64, _I, _P, _P, _P, _P, _I, _I, _P, _P, _I, _P, _P, _I,
+                                     _I, _P, _P, _SZ, _P, _P]
         L.fg8_ep_pack_scales.restype = _I
         L.fg8_ep_pack_scales.argtypes = [_P, _I64, _I64, _P, _P]
         L.fg8_ep_unpack.restype = _I
@@ -303,6 +309,19 @@ def fg8_grouped_gemm_combine(a, sa, b, sb, offsets, M_total, N, K, E, row_token,
                                           _ptr(workspace), ws_bytes, _ptr(dev_status),
                                           _stream(stream)),
            "fg8_grouped_gemm_combine")
+
+
+def fg8_moe_decode_workspace(T: int, k: int, C: int, I: int) -> int:
+    return int(lib().fg8_moe_decode_workspace(T, k, C, I))
+
+
+def fg8_moe_decode(x, T, C, logits, bias, topk_ids, affinity, k, E, wq_up, sw_up, I, wq_dn, sw_dn,
+                   normalize, out_dtype, out, workspace, ws_bytes, dev_status, stream=None):
+    _check(lib().fg8_moe_decode(_ptr(x), T, C, _ptr(logits), _ptr(bias), _ptr(topk_ids),
+                                _ptr(affinity), k, E, _ptr(wq_up), _ptr(sw_up), I, _ptr(wq_dn),
+                                _ptr(sw_dn), normalize, out_dtype, _ptr(out), _ptr(workspace),
+                                ws_bytes, _ptr(dev_status), _stream(stream)),
+           "fg8_moe_decode")
 
 
 def fg8_ep_pack_scales(sa, R, K, sa_rows, stream=None):
@@ -628,6 +647,45 @@ def grouped_gemm_combine(a, sa, b, sb, offsets, row_token, token_row, affinity, 
                              affinity, T, k, int(bool(normalize)), out, workspace,
                              workspace.numel(), st, stream)
     return out
+
+
+def moe_decode_workspace(T, k, C, I, device=None):
+    """A zeroed workspace for moe_decode calls of up to T tokens (kept by the
+    caller: a call leaves it ready for the next)."""
+    n = fg8_moe_decode_workspace(T, k, C, I)
+    if n == 0:
+        raise ValueError("moe_decode takes 1..64 tokens, 1..16 slots and I >= 128")
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def moe_decode(x, wq_up, sw_up, wq_dn, sw_dn, k, logits=None, bias=None, ids=None, affinity=None,
+               normalize=True, out_dtype=FG8_OUT_BF16, out=None, workspace=None, dev_status=None,
+               stream=None):
+    """The expert layer for a few tokens: x bf16 [T, C], the quantized weights
+    (wq_up [E, 2I, C], wq_dn [E, C, I] and their scales) and either logits
+    [T, E] and bias [E] (routing included; ids and affinity are then outputs) or
+    ids int32 [T, k] and affinity fp32 [T, k] -> (out [T, C], ids, affinity)."""
+    T, C = x.shape
+    E, I = wq_up.shape[0], wq_dn.shape[2]
+    dev = x.device
+    f32, u8 = torch.float32, torch.uint8
+    _want("wq_up", wq_up, (E, 2 * I, C), u8)
+    _want("sw_up", sw_up, (E, 2 * I // 128, C // 128), f32)
+    _want("wq_dn", wq_dn, (E, C, I), u8)
+    _want("sw_dn", sw_dn, (E, C // 128, I // 128), f32)
+    _want("logits", logits, (T, E), f32)
+    _want("bias", bias, (E,), f32)
+    if logits is None and (ids is None or affinity is None):
+        raise ValueError("moe_decode needs logits and bias, or ids and affinity")
+    ids = _out(ids, (T, k), torch.int32, dev)
+    affinity = _out(affinity, (T, k), f32, dev)
+    out = _out(out, (T, C), f32 if out_dtype == FG8_OUT_F32 else torch.bfloat16, dev)
+    if workspace is None and T > 0:
+        workspace = moe_decode_workspace(T, k, C, I, dev)
+    fg8_moe_decode(_u16(x), T, C, logits, bias, ids, affinity, k, E, wq_up, sw_up, I, wq_dn, sw_dn,
+                   int(bool(normalize)), out_dtype, out, workspace,
+                   0 if workspace is None else workspace.numel(), dev_status, stream)
+    return out, ids, affinity
 
 
 def unpermute_combine(y, token_row, affinity, normalize=True, out_dtype=FG8_OUT_BF16, out=None,

@@ -491,6 +491,49 @@ fg8_status fg8_grouped_gemm_combine(const uint8_t* a, const float* sa, const uin
                                     size_t ws_bytes, int32_t* dev_status, fg8_stream_t stream);
 
 /*
+ * fg8_moe_decode -- the whole expert layer for a few tokens (a decoding step) in
+ * one kernel: what fg8_route_topk, fg8_quantize_act, the gated up-projection
+ * with its 1x128 quantization, the down-projection and the combine compute one
+ * after the other, for T <= 64 tokens.  Few tokens leave those kernels' 128-row
+ * tiles almost empty and the time to launches; here every weight of the experts
+ * met is streamed once.
+ *     ids, affinity = fg8_route_topk(logits, bias)   (or given: logits NULL)
+ *     xq = 1x128 codes of x                           (fg8_quantize_act's bits)
+ *     [G; U] = Wup[e] xq;  h = silu(G) U, quantized in 1x128 tiles from fp32
+ *     out[t] = sum over the kept slots j of w[t][j] Wdn[e] hq
+ *   with w as in fg8_unpermute_combine.  The experts' rows stay in fp32 until the
+ *   sum.  Sums run in an order that depends on the sizes, the routing and the
+ *   device only: equal calls give equal bits.
+ *   x          bf16 [T][C]
+ *   logits     fp32 [T][E], bias fp32 [E]; or logits NULL (bias is then ignored)
+ *   topk_ids   int32 [T][k], affinity fp32 [T][k]: outputs when logits are given,
+ *              else inputs; an id outside [0, E) drops its slot and writes
+ *              FG8_ERR_BAD_EXPERT_ID to *dev_status.  An expert may fill several
+ *              slots of a token.
+ *   wq_up      E4M3 [E][2I][C] (gate rows, then up rows), sw_up fp32 [E][2I/128][C/128]
+ *   wq_dn      E4M3 [E][C][I], sw_dn fp32 [E][C/128][I/128]
+ *   out        bf16 or fp32 [T][C] (out_dtype), written in full
+ *   workspace  >= fg8_moe_decode_workspace(T, k, C, I) bytes, 16-byte aligned,
+ *              whose first FG8_MOE_DECODE_HEAD bytes are zero before the first
+ *              call.  A call leaves them ready for the next one of any size; after
+ *              one that reported FG8_ERR_TIMEOUT they are to be zeroed again.
+ *              Calls that overlap on the GPU need their own workspace
+ *              (FG8_ERR_WORKSPACE_SHARED where that is noticed).
+ *   T <= 64, 1 <= k <= min(16, E), E <= 1024, C % 128 == 0, I % 128 == 0;
+ *   x, wq_up, wq_dn, out 16-byte aligned.  NaN logits are outside the contract.
+ *   A cooperative launch (one CTA per SM); every wait is bounded
+ *   (FG8_ERR_TIMEOUT in *dev_status).
+ */
+#define FG8_MOE_DECODE_HEAD 4096
+size_t fg8_moe_decode_workspace(int64_t T, int k, int64_t C, int64_t I);
+fg8_status fg8_moe_decode(const uint16_t* x, int64_t T, int C, const float* logits,
+                          const float* bias, int32_t* topk_ids, float* affinity, int k, int E,
+                          const uint8_t* wq_up, const float* sw_up, int I, const uint8_t* wq_dn,
+                          const float* sw_dn, int normalize, int out_dtype, void* out,
+                          void* workspace, size_t ws_bytes, int32_t* dev_status,
+                          fg8_stream_t stream);
+
+/*
  * Expert-parallel exchange of FP8 rows (the data plane around an all-to-all;
  * [DS] sec. 2.2: training on a cluster of NVLink / InfiniBand nodes with FP8
  * communication, and the experts spread over the GPUs).  With W ranks, rank

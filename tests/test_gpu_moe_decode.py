@@ -1,0 +1,282 @@
+"""The few-token expert layer in one kernel against the layer in 64 bits and
+against the chain of kernels that computes it for many tokens.
+
+The input's codes are the quantizer's own (bit-equal, so they carry no error
+here).  Reference: [G; U] in 64 bits from the dequantized operands; h = silu(G) U
+quantized to E4M3 in 1x128 tiles; out = sum_j w_j Wdn hq.
+
+Tolerance, per output element.  A GEMM value (tensor-core partial of 128 products,
+fp32 promotion over the blocks) is off by at most D = (128 + blocks) 2^-24 of
+sum |a b|; through silu(G) U (slope of silu at most 1.1, fast exponential and
+division 2^-20) h is off by dh, and h / scale by dz.  A code of h then equals the
+reference's unless h / scale lies within 2 dz of a rounding midpoint, where it may
+be one step away.  So out is off by at most
+    sum_j w_j sum_i |Wdn_i| (step_i [midpoint in reach] + scale's own error)
+    + D2 sum_j w_j sum_i |Wdn_i hq_i|,  D2 = (128 + 2 blocks + k + 8) 2^-24,
+and half a step of the output's type."""
+
+import numpy as np
+import pytest
+import torch
+
+from fp8_fine_grained_permute_b200 import build as fbuild
+from fp8_fine_grained_permute_b200 import fg8
+from fp8_fine_grained_permute_b200 import workloads as W
+
+pytestmark = pytest.mark.gpu
+
+EPS = 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    fbuild.build()
+    fg8.lib()
+    torch.cuda.init()
+
+
+class Layer:
+    def __init__(self, E, C, I, seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        n = lambda *s: torch.randn(s, generator=g, device="cuda")   # noqa: E731
+        self.E, self.C, self.I = E, C, I
+        self.wq_up, self.sw_up = fg8.quantize_weight((n(E, 2 * I, C) * (1.5 / C ** 0.5)).to(torch.bfloat16))
+        self.wq_dn, self.sw_dn = fg8.quantize_weight((n(E, C, I) * (1.0 / I ** 0.5)).to(torch.bfloat16))
+        self.g = g
+
+    def weights(self):
+        return self.wq_up, self.sw_up, self.wq_dn, self.sw_dn
+
+    def x(self, T):
+        return torch.randn(T, self.C, generator=self.g, device="cuda").to(torch.bfloat16)
+
+    def routing(self, T):
+        return (torch.randn(T, self.E, generator=self.g, device="cuda"),
+                0.2 * torch.rand(self.E, generator=self.g, device="cuda") - 0.1)
+
+
+def _deq_block(q, s):
+    return q.view(torch.float8_e4m3fn).double() * s.double().repeat_interleave(128, 0).repeat_interleave(128, 1)
+
+
+def _half_step(z):
+    a = z.abs().clamp(min=2.0 ** -6)
+    return 0.5 * torch.exp2(torch.floor(torch.log2(a)) - 3)
+
+
+def _e4m3(z):
+    """Nearest E4M3 value in 64 bits (ties to even)."""
+    st = 2 * _half_step(z)
+    return (torch.round(z / st) * st).clamp(-448, 448)
+
+
+def reference(L, x, ids, aff, normalize=True):
+    """-> (out, bound without the output's own rounding), fp64 [T, C]."""
+    T, k = ids.shape
+    xq, sx = fg8.quantize_act_rows(x)
+    xd = xq.view(torch.float8_e4m3fn).double() * sx.double().t().repeat_interleave(128, 1)
+    kept = (ids >= 0) & (ids < L.E)
+    a = torch.where(kept, aff.double(), 0.0)
+    s = a.sum(1, keepdim=True)
+    w = torch.where(s != 0, a / s, 0.0) if normalize else a
+    out = torch.zeros(T, L.C, dtype=torch.float64, device="cuda")
+    bound = torch.zeros_like(out)
+    I = L.I
+    D, D2 = (128 + L.C // 128) * EPS, (128 + 2 * I // 128 + k + 8) * EPS
+    for e in torch.unique(ids[kept]).tolist():
+        t, j = (ids == e).nonzero(as_tuple=True)
+        Wu, Wd = _deq_block(L.wq_up[e], L.sw_up[e]), _deq_block(L.wq_dn[e], L.sw_dn[e])
+        gu, mag = xd[t] @ Wu.t(), xd[t].abs() @ Wu.abs().t()
+        g, u = gu[:, :I], gu[:, I:]
+        sig = torch.sigmoid(g)
+        h = g * sig * u
+        # silu' <= 1.1; fast exp and division: 2^-20 relative
+        dh = 1.1 * u.abs() * D * mag[:, :I] + (g * sig).abs() * D * mag[:, I:] + 2.0 ** -20 * h.abs()
+        amax = h.abs().view(-1, I // 128, 128).amax(2)
+        sc = torch.where(amax > 0, amax / 448, 1.0).repeat_interleave(128, 1)
+        dmax = dh.view(-1, I // 128, 128).amax(2).repeat_interleave(128, 1)
+        z = h / sc
+        q = _e4m3(z)
+        # a scale off by dmax / 448 moves z by |z| dmax / amax
+        dz = dh / sc + z.abs() * (dmax / (448 * sc) + 2 * EPS)
+        reach = _half_step(z) - (z - q).abs() <= 2 * dz
+        dq = torch.where(reach, 2 * _half_step(z), 0.0) * sc + q.abs() * (dmax / 448 + 2 * EPS * sc)
+        hq = q * sc
+        wt = w[t, j][:, None]
+        out.index_add_(0, t, wt * (hq @ Wd.t()))
+        bound.index_add_(0, t, wt * (dq @ Wd.abs().t() + D2 * (hq.abs() @ Wd.abs().t())))
+    return out, bound
+
+
+def check(L, x, ids, aff, out, normalize=True):
+    ref, bound = reference(L, x, ids, aff, normalize)
+    err = (out.double() - ref).abs()
+    half = 2.0 ** -8 if out.dtype == torch.bfloat16 else EPS
+    lim = bound + half * (ref.abs() + bound) + 1e-30
+    assert torch.all(err <= lim), f"{(err / lim).max().item()} of the limit"
+
+
+def run(L, x, k, ws=None, **kw):
+    st = fg8.new_status()
+    out, ids, aff = fg8.moe_decode(x, *L.weights(), k, workspace=ws, dev_status=st, **kw)
+    torch.cuda.synchronize()
+    assert st.item() == 0, st.item()
+    return out, ids, aff
+
+
+CASES = [  # T, E, k, C, I
+    (1, 4, 1, 128, 128), (1, 64, 6, 2048, 768), (2, 3, 3, 256, 384), (5, 8, 2, 640, 128),
+    (16, 4, 4, 384, 256), (17, 4, 2, 256, 256), (33, 5, 1, 512, 640), (64, 8, 8, 256, 256),
+    (64, 1, 1, 384, 128), (40, 100, 7, 128, 384), (3, 1000, 16, 256, 128), (11, 64, 6, 1024, 512)]
+
+
+@pytest.mark.parametrize("T,E,k,C,I", CASES)
+@pytest.mark.parametrize("f32", [False, True])
+def test_layer_matches_formula(T, E, k, C, I, f32):
+    L = Layer(E, C, I, seed=T * 7 + E)
+    x = L.x(T)
+    logits, bias = L.routing(T)
+    out, ids, aff = run(L, x, k, logits=logits, bias=bias, out_dtype=fg8.FG8_OUT_F32 if f32 else fg8.FG8_OUT_BF16)
+    rid, raff = fg8.route_topk(logits, bias, k)
+    assert torch.equal(ids, rid) and torch.equal(aff, raff)
+    check(L, x, ids, aff, out)
+
+
+def test_given_routing_bad_ids_repeated_experts_and_no_normalization():
+    L = Layer(6, 384, 256, seed=2)
+    T, k = 20, 4
+    x = L.x(T)
+    ids = torch.randint(0, 6, (T, k), device="cuda", dtype=torch.int32)   # repeats happen
+    ids[3] = 2                                  # one expert in every slot
+    aff = torch.rand(T, k, device="cuda") + 0.01
+    aff[5] = 0                                  # affinities that sum to 0: zeros when normalized
+    for normalize in (True, False):
+        out, _, _ = run(L, x, k, ids=ids, affinity=aff, normalize=normalize, out_dtype=fg8.FG8_OUT_F32)
+        check(L, x, ids, aff, out, normalize)
+    bad = ids.clone()
+    bad[0, 1], bad[7], bad[9, 0] = -1, 6, 1 << 20
+    st = fg8.new_status()
+    out, _, _ = fg8.moe_decode(x, *L.weights(), k, ids=bad, affinity=aff, dev_status=st, out_dtype=fg8.FG8_OUT_F32)
+    torch.cuda.synchronize()
+    assert st.item() == fg8.FG8_ERR_BAD_EXPERT_ID
+    assert torch.all(out[7] == 0) and torch.all(out[5] == 0)
+    check(L, x, bad, aff, out)
+
+
+def test_no_valid_expert_and_no_tokens():
+    L = Layer(2, 256, 128, seed=3)
+    x = L.x(3)
+    ids = torch.full((3, 2), -1, device="cuda", dtype=torch.int32)
+    st = fg8.new_status()
+    out, _, _ = fg8.moe_decode(x, *L.weights(), 2, ids=ids, affinity=torch.ones(3, 2, device="cuda"), dev_status=st,
+                               out=torch.full((3, 256), 7.0, device="cuda", dtype=torch.bfloat16))
+    torch.cuda.synchronize()
+    assert st.item() == fg8.FG8_ERR_BAD_EXPERT_ID and torch.all(out == 0)
+    out, ids, _ = fg8.moe_decode(x[:0], *L.weights(), 2, ids=ids[:0], affinity=torch.ones(0, 2, device="cuda"))
+    assert out.shape == (0, 256)
+
+
+def test_all_tokens_on_one_expert():
+    """More tokens than a group holds, every one of them on the same experts."""
+    L = Layer(4, 512, 256, seed=4)
+    x = L.x(64)
+    ids = torch.tensor([[3, 1]], device="cuda", dtype=torch.int32).repeat(64, 1)
+    aff = torch.rand(64, 2, device="cuda") + 0.1
+    out, _, _ = run(L, x, 2, ids=ids, affinity=aff, out_dtype=fg8.FG8_OUT_F32)
+    check(L, x, ids, aff, out)
+
+
+def test_equal_calls_equal_bits_on_one_workspace_of_many_sizes():
+    """One workspace, zeroed once, through calls of different sizes; results repeat."""
+    ws = fg8.moe_decode_workspace(64, 8, 2048, 768)
+    La, Lb = Layer(16, 1024, 768, seed=5), Layer(5, 256, 128, seed=6)
+    xa, xb = La.x(50), Lb.x(3)
+    ra, rb = La.routing(50), Lb.routing(3)
+    first = None
+    for _ in range(4):
+        oa, _, _ = run(La, xa, 8, ws=ws, logits=ra[0], bias=ra[1], out_dtype=fg8.FG8_OUT_F32)
+        ob, _, _ = run(Lb, xb, 2, ws=ws, logits=rb[0], bias=rb[1], out_dtype=fg8.FG8_OUT_F32)
+        if first is None:
+            first = oa.clone(), ob.clone()
+        assert torch.equal(oa, first[0]) and torch.equal(ob, first[1])
+    head = ws[:fg8.FG8_MOE_DECODE_HEAD].view(torch.int32)
+    assert head[0].item() == 0 and torch.all(head[16:16 + 160] == 0)
+
+
+def test_close_to_the_chain_of_kernels():
+    """The same layer through the many-token kernels: they differ by the chain's
+    bf16 rows between the down-projection and the combine (2^-8 each at most)
+    and by codes of h at rounding midpoints."""
+    L = Layer(64, 2048, 768, seed=7)
+    T, k = 24, 6
+    x = L.x(T)
+    logits, bias = L.routing(T)
+    out, ids, aff = run(L, x, k, logits=logits, bias=bias, out_dtype=fg8.FG8_OUT_F32)
+    act = fg8.route_quantize_act(logits, bias, x, k)
+    hq, sh = fg8.grouped_gemm_swiglu_quant(act["xq"], act["sa"], L.wq_up, L.sw_up, act["offsets"])
+    y = fg8.grouped_gemm(hq, sh, L.wq_dn, L.sw_dn, act["offsets"])
+    want = fg8.unpermute_combine(y, act["token_row"], act["affinity"], out_dtype=fg8.FG8_OUT_F32)
+    assert torch.equal(ids, act["ids"])
+    assert ((out - want).norm() / want.norm()).item() <= 2.0 ** -8
+
+
+def test_captured_graphs_share_a_workspace_and_a_side_stream():
+    L = Layer(8, 512, 256, seed=8)
+    ws = fg8.moe_decode_workspace(32, 4, 512, 256)
+    st = fg8.new_status()
+    s = torch.cuda.Stream()
+    graphs = []
+    for T in (1, 20):
+        x, (logits, bias) = L.x(T), L.routing(T)
+        bufs = dict(out=torch.empty(T, 512, device="cuda"), ids=torch.empty(T, 4, device="cuda", dtype=torch.int32),
+                    affinity=torch.empty(T, 4, device="cuda"))
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            fg8.moe_decode(x, *L.weights(), 4, logits=logits, bias=bias, out_dtype=fg8.FG8_OUT_F32, workspace=ws,
+                           dev_status=st, **bufs)
+        graphs.append((g, x, logits, bias, bufs))
+    for rep in range(3):
+        for g, x, logits, bias, bufs in graphs:
+            x.copy_(L.x(x.shape[0]))
+            logits.copy_(L.routing(x.shape[0])[0])
+            g.replay()
+            torch.cuda.synchronize()
+            assert st.item() == 0
+            check(L, x, bufs["ids"], bufs["affinity"], bufs["out"])
+
+
+def test_two_calls_at_once_on_their_own_workspaces():
+    L = Layer(32, 1024, 512, seed=9)
+    T, k = 30, 4
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    xs = [L.x(T) for _ in streams]
+    rs = [L.routing(T) for _ in streams]
+    ws = [fg8.moe_decode_workspace(T, k, 1024, 512) for _ in streams]
+    st = [fg8.new_status() for _ in streams]
+    want = [run(L, x, k, logits=r[0], bias=r[1])[0].clone() for x, r in zip(xs, rs)]
+    torch.cuda.synchronize()
+    outs = [torch.empty(T, 1024, device="cuda", dtype=torch.bfloat16) for _ in streams]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                fg8.moe_decode(xs[i], *L.weights(), k, logits=rs[i][0], bias=rs[i][1], out=outs[i], workspace=ws[i],
+                               dev_status=st[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert st[i].item() == 0 and torch.equal(outs[i], want[i])
+
+
+def test_saturating_inputs():
+    """Tokens of very different sizes in one batch, zeros among them."""
+    L = Layer(4, 256, 256, seed=10)
+    x = L.x(6)
+    x[0] *= 300.0
+    x[1] *= 1e-6
+    x[2] = 0
+    ids = torch.tensor([[0, 1]] * 6, device="cuda", dtype=torch.int32)
+    aff = torch.rand(6, 2, device="cuda") + 0.1
+    out, _, _ = run(L, x, 2, ids=ids, affinity=aff, out_dtype=fg8.FG8_OUT_F32)
+    assert torch.all(out[2] == 0)
+    for t in range(6):
+        check(L, x[t:t + 1], ids[t:t + 1], aff[t:t + 1], out[t:t + 1])
