@@ -61,6 +61,38 @@ constexpr uint32_t kABytes = 2 * 128 * 128;          // a step's weights
 constexpr int kTmemBufs = 4;
 constexpr int kFillWarps = 4;
 
+// Contiguous shares of `total` equal steps: the first `rem` CTAs have q + 1, the
+// others up to `ctas` q.  No more CTAs take part than there are steps, so that
+// every CTA from a unit's first to its last has a part of it.
+struct Share {
+    int total, ctas, q, rem;
+    FG8_DEV int begin(int c) const { return c >= ctas ? total : c * q + min(c, rem); }
+    FG8_DEV int owner(int step) const {
+        const int big = rem * (q + 1);
+        return step < big ? step / (q + 1) : rem + (step - big) / q;
+    }
+};
+FG8_DEV Share make_share(int total, int all) {
+    Share s;
+    s.total = total;
+    s.ctas = min(total, all);
+    s.q = total / max(1, s.ctas);
+    s.rem = total - s.q * s.ctas;
+    return s;
+}
+
+// Where a CTA's share of a projection begins and ends, and what steps are there:
+// up-projection: unit a (group c, h block d), K block b; down-projection: output
+// block a, inside it group c, pair of K blocks d.
+struct Cursor {
+    int step, a, b, c, d;
+};
+struct Plan {
+    int G;
+    Share up, dn;
+    Cursor cur[4];   // up begin, up end, down begin, down end
+};
+
 // Variants: N tokens a group.  N = 16 when T <= 16 (an expert then rarely has
 // more tokens and the ring is a stage deeper), else 32.
 template <int N>
@@ -68,37 +100,44 @@ struct Cfg {
     static constexpr int kStages = N == 16 ? 5 : 4;
     static constexpr uint32_t kBBytes = 2 * N * 128;             // two K blocks of B (the first alone in the up-projection)
     static constexpr uint32_t kStage = kABytes + kBBytes;
-    static constexpr int kTokens = N == 16 ? 16 : kMaxT;         // rows of the output accumulator
+    static constexpr int kTokens = N == 16 ? 16 : kMaxT;
     static constexpr int kPairs = kTokens * fg8::kRouteMaxK;
+    static constexpr int kAccRows = kTokens > 2 * N ? kTokens : 2 * N;   // a group's gate and up, or the tokens' sums
     // factor slots: written for step n while steps up to n - kStages - kTmemBufs
     // have been promoted (their stage and partial buffer were free again)
     static constexpr int kSlots = kStages + kTmemBufs;
     static constexpr uint32_t kTmemCols = kTmemBufs * 2 * N;     // 128 or 256
-    static constexpr uint32_t kOffAcc = kStages * kStage;        // float [kTokens][128]
-    static constexpr uint32_t kOffFactors = kOffAcc + kTokens * 512;
+    static constexpr uint32_t kOffAcc = kStages * kStage;        // float [kAccRows][128]
+    static constexpr uint32_t kOffFactors = kOffAcc + kAccRows * 512;
     static constexpr uint32_t kOffRed = kOffFactors + kSlots * 2 * N * 4;   // float [2][4][N]
     static constexpr uint32_t kOffBars = kOffRed + 2 * 4 * N * 4;
-    static constexpr int kNumBars = 2 * kStages + 2 * kTmemBufs + 1 + 1;    // full, empty, tfull, tempty, drain, group
-    static constexpr uint32_t kOffMisc = kOffBars + 8 * kNumBars;           // tmem slot, abort, generation, last[2]
-    static constexpr uint32_t kOffGroups = kOffMisc + 32;        // uint32 [kPairs]: n | first << 6 | expert << 16
-    static constexpr uint32_t kOffList = kOffGroups + 4 * kPairs;   // uint16 [kPairs]: pair, experts ascending
-    static constexpr uint32_t kOffW = kOffList + 2 * kPairs;     // float [kPairs]: gate weight of a pair
-    static constexpr uint32_t kOffIds = kOffW + 4 * kPairs;      // int32 [kPairs]
-    static constexpr uint32_t kOffCnt = kOffIds + 4 * kPairs;    // int32 [kMaxE + 1]
-    static constexpr uint32_t kOffWarp = kOffCnt + 4 * (kMaxE + 4);   // int32 [36]
-    static constexpr uint32_t kSmem = kOffWarp + 4 * 36 + 1024;  // + alignment slack
+    static constexpr int kNumBars = 2 * kStages + 2 * kTmemBufs + 3;    // full, empty, tfull, tempty, drain, group, h
+    static constexpr uint32_t kOffMisc = kOffBars + 8 * kNumBars;           // tmem slot, abort, call number, last[2]
+    static constexpr uint32_t kOffPlan = kOffMisc + 32;
+    static constexpr uint32_t kOffGroups = kOffPlan + 128;        // uint32 [kPairs]: n | first << 6 | expert << 16
+    static constexpr uint32_t kOffList = kOffGroups + 4 * kPairs;   // uint32 [kPairs]: pair | token << 16, experts ascending
+    static constexpr uint32_t kOffW = kOffList + 4 * kPairs;     // float [kPairs]: gate weight of a pair
+    static constexpr uint32_t kOffAff = kOffW + 4 * kPairs;      // float [kPairs]
+    static constexpr uint32_t kOffIds = kOffAff + 4 * kPairs;      // int32 [kPairs]
+    static constexpr uint32_t kOffMet = kOffIds + 4 * kPairs;    // uint16 [kPairs]: experts met, by first pair
+    static constexpr uint32_t kOffCnt = kOffMet + 2 * kPairs;    // int32 [kMaxE]: pairs, then first place in the list
+    static constexpr uint32_t kSmem = kOffCnt + 4 * kMaxE + 1024;   // + alignment slack
     static_assert(kSmem <= 232448, "shared memory per CTA");
     static_assert(kStage % 1024 == 0, "swizzle atoms");
+    static_assert(sizeof(Plan) <= 128, "plan");
 };
 
 // workspace: a fixed head of counters (zero between calls), then h, its scales
 // and the partials of cut units
 constexpr size_t kHeadBytes = FG8_MOE_DECODE_HEAD;
 struct Head {
-    uint32_t bar_count, bar_gen;
-    uint32_t pad[14];
-    uint32_t up_count[kMaxCtas];     // by the unit's first CTA
-    uint32_t down_count[kMaxCtas];   // by the unit's first CTA, cleared at the start of a call
+    // call numbers order the arrivals, so nothing is cleared between calls: a
+    // CTA's h is written (the grid barrier); its part of the output block that it
+    // shares with earlier [0] or later [1] CTAs is written
+    uint32_t h_done;                 // all CTAs' arrivals of all calls
+    uint32_t calls[kMaxCtas];        // calls that the CTA has finished
+    uint32_t part_done[kMaxCtas][2];
+    uint32_t up_count[kMaxCtas];     // by the unit's first CTA; 0 between calls
 };
 static_assert(sizeof(Head) <= kHeadBytes, "counter head");
 
@@ -111,6 +150,7 @@ struct Args {
     const float* sw_up;      // [E][2 I / 128][C / 128]
     const float* sw_dn;      // [E][C / 128][I / 128]
     int T, k, E, C, I;
+    uint32_t k_magic;        // ceil(2^32 / k), 0 for k = 1: pair / k by multiplication
     int normalize, out_f32;
     void* out;
     Head* head;
@@ -139,16 +179,141 @@ FG8_DEV void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) {
         : "memory");
 }
 
-// Contiguous shares of `total` equal steps: CTA c has [begin(c), begin(c + 1)).
-// No more CTAs take part than there are steps, so that every CTA from a unit's
-// first to its last has a part of it.
-struct Share {
-    int64_t total;
-    int ctas;
-    FG8_DEV Share(int64_t n, int all) : total(n), ctas((int)min(n, (int64_t)all)) {}
-    FG8_DEV int64_t begin(int c) const { return c >= ctas ? total : total * c / ctas; }
-    FG8_DEV int owner(int64_t step) const { return (int)(((step + 1) * ctas - 1) / total); }
-};
+FG8_DEV void st_release_gpu(uint32_t* p, uint32_t v) {
+    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+
+FG8_DEV void red_release_gpu(uint32_t* p, uint32_t v) {
+    asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+
+// A warp waits until flags[0], flags[stride], .. (n of them) hold `call` (bounded:
+// raises the abort flag and reports FG8_ERR_TIMEOUT).
+FG8_DEV void wait_calls(const uint32_t* flags, int stride, int n, uint32_t call, int lane, volatile int* abort_flag,
+                        int32_t* status) {
+    const uint64_t t0 = fg8::globaltimer_ns();
+    for (int i = lane; i < n; i += 32) {
+        while (fg8::ld_acquire_gpu(flags + i * stride) != call) {
+            if (*abort_flag) break;
+            if (fg8::globaltimer_ns() - t0 > fg8::kWaitLimitNs) {
+                fg8::set_status(status, FG8_ERR_TIMEOUT);
+                *abort_flag = 1;
+                break;
+            }
+        }
+    }
+    __syncwarp();
+}
+
+// E4M3 codes of 8 bf16 values over their tile's scale: the quotient as product,
+// residual and correction.  For every pair of a bf16 magnitude and a tile maximum
+// it rounds to the code that the IEEE quotient gives (checked over all mantissas
+// and 30 binades, with reciprocals up to 2 units off), and it takes a tenth of
+// the division's instructions: code size is latency here.  Scales below 2^-100
+// take the division.  The order of the terms keeps the sign of a zero.
+FG8_DEV uint2 quant8_corrected(const uint4& v, float s) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t c[4];
+    if (s >= 0x1p-100f) {
+        const float r = fg8::inv_scale(s);
+        const float2 nr = make_float2(-r, -r), s2 = make_float2(s, s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 nx = make_float2(-fg8::bf16_lo(w[i]), -fg8::bf16_hi(w[i]));
+            const float2 z0 = __fmul2_rn(nx, nr);
+            const float2 z = __ffma2_rn(__ffma2_rn(z0, s2, nx), nr, z0);
+            c[i] = fg8::cvt_e4m3x2(z.x, z.y);
+        }
+    } else {
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i)
+            c[i] = fg8::cvt_e4m3x2(__fdiv_rn(fg8::bf16_lo(w[i]), s), __fdiv_rn(fg8::bf16_hi(w[i]), s));
+    }
+    return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+// One fp32 value over its tile's scale, likewise (to 2^-45 before the rounding).
+FG8_DEV uint32_t code_of(float x, float s) {
+    float z;
+    if (s >= 0x1p-100f) {
+        const float r = fg8::inv_scale(s);
+        const float z0 = __fmul_rn(x, r);
+        z = __fmaf_rn(__fmaf_rn(z0, s, -x), -r, z0);
+    } else {
+        z = __fdiv_rn(x, s);
+    }
+    return fg8::cvt_e4m3x2(z, 0.f) & 0xFFu;
+}
+
+// fg8::route_token's choice with warp reductions on keys that order like the
+// scores (0: taken, or no expert); lane j < k ends with the j-th chosen expert
+// and its affinity.
+template <int PER_LANE>
+FG8_DEV void route_token_keys(const float (&lu)[PER_LANE], const float (&lb)[PER_LANE], int E, int k, int lane,
+                              int32_t& id, float& affinity) {
+    uint32_t key[PER_LANE];
+#pragma unroll
+    for (int i = 0; i < PER_LANE; ++i) {
+        const uint32_t b = __float_as_uint(__fadd_rn(fg8::route_sigmoid(lu[i]), lb[i]));
+        key[i] = lane + 32 * i < E ? (b & 0x80000000u ? ~b : b | 0x80000000u) : 0u;
+    }
+    id = 0;
+#pragma unroll 1
+    for (int j = 0; j < k; ++j) {
+        uint32_t best = key[0];
+#pragma unroll
+        for (int i = 1; i < PER_LANE; ++i) best = max(best, key[i]);
+        const uint32_t top = __reduce_max_sync(kFull, best);
+        int e = INT_MAX;   // lowest expert with it
+#pragma unroll
+        for (int i = PER_LANE - 1; i >= 0; --i)
+            if (key[i] == top) e = lane + 32 * i;
+        e = __reduce_min_sync(kFull, e);
+#pragma unroll
+        for (int i = 0; i < PER_LANE; ++i)
+            if (lane + 32 * i == e) key[i] = 0u;
+        if (lane == j) id = e;
+    }
+    float u = 0.f;
+#pragma unroll
+    for (int i = 0; i < PER_LANE; ++i) {
+        const float v = __shfl_sync(kFull, lu[i], id & 31);
+        if (id >> 5 == i) u = v;
+    }
+    affinity = fg8::route_sigmoid(u);
+}
+
+// The tokens t = warp, warp + kThreads / 32, ... of a CTA, a warp each, the next
+// token's logits ahead.
+template <int PER_LANE>
+FG8_DEV void route_tokens(const Args& a, int warp, int lane, int32_t* s_ids, float* s_aff, bool write) {
+    float lu[PER_LANE], lb[PER_LANE], nu[PER_LANE];
+    auto load = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < PER_LANE; ++i)
+            nu[i] = t < a.T && lane + 32 * i < a.E ? __ldg(a.logits + (int64_t)t * a.E + lane + 32 * i) : 0.f;
+    };
+    load(warp);
+#pragma unroll
+    for (int i = 0; i < PER_LANE; ++i) lb[i] = lane + 32 * i < a.E ? __ldg(a.bias + lane + 32 * i) : 0.f;
+#pragma unroll 1
+    for (int t = warp; t < a.T; t += kThreads / 32) {
+#pragma unroll
+        for (int i = 0; i < PER_LANE; ++i) lu[i] = nu[i];
+        load(t + kThreads / 32);
+        int32_t id;
+        float s;
+        route_token_keys<PER_LANE>(lu, lb, a.E, a.k, lane, id, s);
+        if (lane < a.k) {
+            s_ids[t * a.k + lane] = id;
+            s_aff[t * a.k + lane] = s;
+            if (write) {
+                a.ids[t * a.k + lane] = id;
+                a.affinity[t * a.k + lane] = s;
+            }
+        }
+    }
+}
 
 template <int N>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -165,16 +330,19 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
     auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * S + b); };
     auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * S + kTmemBufs + b); };
     const uint32_t drain_bar = bar0 + 8u * (2 * S + 2 * kTmemBufs);
-    const uint32_t group_bar = drain_bar + 8u;
+    const uint32_t group_bar = drain_bar + 8u, h_bar = drain_bar + 16u;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + K::kOffMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + K::kOffMisc + 4);
-    volatile uint32_t* s_gen = reinterpret_cast<volatile uint32_t*>(smem + K::kOffMisc + 8);
+    volatile uint32_t* s_call = reinterpret_cast<volatile uint32_t*>(smem + K::kOffMisc + 8);
     volatile int* s_last = reinterpret_cast<volatile int*>(smem + K::kOffMisc + 16);   // [2]
     uint32_t* s_groups = reinterpret_cast<uint32_t*>(smem + K::kOffGroups);
-    uint16_t* s_list = reinterpret_cast<uint16_t*>(smem + K::kOffList);
+    uint32_t* s_list = reinterpret_cast<uint32_t*>(smem + K::kOffList);
     float* s_w = reinterpret_cast<float*>(smem + K::kOffW);
+    float* s_aff = reinterpret_cast<float*>(smem + K::kOffAff);
     int32_t* s_ids = reinterpret_cast<int32_t*>(smem + K::kOffIds);
     int32_t* s_cnt = reinterpret_cast<int32_t*>(smem + K::kOffCnt);
+    uint16_t* s_met = reinterpret_cast<uint16_t*>(smem + K::kOffMet);
+    Plan& plan = *reinterpret_cast<Plan*>(smem + K::kOffPlan);
     float* s_factors = reinterpret_cast<float*>(smem + K::kOffFactors);
     float* s_acc = reinterpret_cast<float*>(smem + K::kOffAcc);
     float* s_red = reinterpret_cast<float*>(smem + K::kOffRed);
@@ -184,8 +352,9 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
     const int CB = a.C / 128, IB = a.I / 128, IB2 = (IB + 1) / 2;
     const int R = a.T * a.k;
 
-    // ------------------------------------------------------------ set-up
-    if (tid == 0) {
+    // ------------------------------------------------------------ set-up and routing
+    // every CTA routes every token: cheaper than a second grid barrier
+    if (tid == 64) {
         for (int s = 0; s < S; ++s) {
             mbar_init(full_bar(s), 2);      // weight producer (with the bytes), fill warp
             mbar_init(empty_bar(s), 1);
@@ -196,10 +365,9 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
         }
         mbar_init(drain_bar, 1);
         mbar_init(group_bar, 4);
+        mbar_init(h_bar, 1);
         *abort_flag = 0;
-        // before this CTA arrives at the grid barrier its generation cannot change
-        *s_gen = fg8::ld_acquire_gpu(&a.head->bar_gen);
-        a.head->down_count[cta] = 0;
+        *s_call = a.head->calls[cta] + 1u;
         fence_barrier_init();
     }
     if (warp == 1) {
@@ -208,34 +376,15 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    for (int e = tid; e <= a.E; e += kThreads) s_cnt[e] = 0;
-
-    // ------------------------------------------------------------ routing
-    // every CTA routes every token: cheaper than a second grid barrier
-    float* s_aff = s_w;   // turned into weights below
+    if (tid == 96) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_up)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_dn)) : "memory");
+    }
     if (a.logits) {
-        auto route = [&](auto per_lane) {
-            constexpr int PL = decltype(per_lane)::value;
-            float bl[PL];
-#pragma unroll
-            for (int i = 0; i < PL; ++i) bl[i] = lane + 32 * i < a.E ? a.bias[lane + 32 * i] : 0.f;
-            for (int t = warp; t < a.T; t += kThreads / 32) {
-                int32_t id;
-                float s;
-                fg8::route_token<PL>(a.logits + (int64_t)t * a.E, bl, a.E, a.k, lane, id, s);
-                if (lane < a.k) {
-                    s_ids[t * a.k + lane] = id;
-                    s_aff[t * a.k + lane] = s;
-                    if (cta == 0) {
-                        a.ids[t * a.k + lane] = id;
-                        a.affinity[t * a.k + lane] = s;
-                    }
-                }
-            }
-        };
-        if (a.E <= 64) route(std::integral_constant<int, 2>());
-        else if (a.E <= 256) route(std::integral_constant<int, 8>());
-        else route(std::integral_constant<int, 32>());
+        // warp 0 has no other set-up: with one token it starts on it at once
+        if (a.E <= 64) route_tokens<2>(a, warp, lane, s_ids, s_aff, cta == 0);
+        else if (a.E <= 256) route_tokens<8>(a, warp, lane, s_ids, s_aff, cta == 0);
+        else route_tokens<32>(a, warp, lane, s_ids, s_aff, cta == 0);
     } else {
         for (int p = tid; p < R; p += kThreads) {
             int32_t id = a.ids[p];
@@ -247,60 +396,100 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
             s_aff[p] = a.affinity[p];
         }
     }
-    __syncthreads();
-    // a pair's place among its expert's pairs, in pair order: every CTA has to get
-    // the same lists (they index the partials that CTAs join), so one warp counts
-    if (warp == 0) {
-        for (int p0 = 0; p0 < R; p0 += 32) {
-            const int p = p0 + lane, id = p < R ? s_ids[p] : -1;
-            const unsigned same = __match_any_sync(kFull, id);
-            const int before = id >= 0 ? s_cnt[id] : 0;
-            __syncwarp();
-            if (id >= 0) {
-                const int rank = __popc(same & ((1u << lane) - 1u));
-                s_ids[p] = id | ((before + rank) << 10);
-                if (rank == 0) s_cnt[id] = before + __popc(same);
-            }
-            __syncwarp();
-        }
-    }
-    __syncthreads();
-    // one thread a token: its gate weights, as fg8_unpermute_combine
-    if (a.normalize && tid < a.T) {
-        float sum = 0.f;
-        for (int j = 0; j < a.k; ++j)
-            if (s_ids[tid * a.k + j] >= 0) sum = __fadd_rn(sum, s_aff[tid * a.k + j]);
-        for (int j = 0; j < a.k; ++j)
-            s_w[tid * a.k + j] = sum != 0.f ? __fdiv_rn(s_aff[tid * a.k + j], sum) : 0.f;
-    }
-    // exclusive prefix of pairs (low half) and of groups (high half) over experts
-    for (int e = tid; e < a.E; e += kThreads) {
-        const int c = s_cnt[e];
-        s_cnt[e] = c | ((c + N - 1) / N << 16);
-    }
-    __syncthreads();
-    fg8::block_exclusive_scan(s_cnt, s_cnt, a.E, reinterpret_cast<int32_t*>(smem + K::kOffWarp));
-    for (int p = tid; p < R; p += kThreads) {
-        const int v = s_ids[p];
-        if (v >= 0) s_list[(s_cnt[v & 1023] & 0xFFFF) + (v >> 10)] = (uint16_t)p;
-    }
-    for (int e = tid; e < a.E; e += kThreads) {
-        const int lo = s_cnt[e], hi = s_cnt[e + 1];
-        int first = lo & 0xFFFF;
-        const int end = hi & 0xFFFF;
-        for (int g = lo >> 16; g < (hi >> 16); ++g, first += N)
-            s_groups[g] = (uint32_t)min(N, end - first) | ((uint32_t)first << 6) | ((uint32_t)e << 16);
-    }
-    const int G = s_cnt[a.E] >> 16;
+    for (int e = tid; e < a.E; e += kThreads) s_cnt[e] = 0;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
+    auto token_of = [&](int p) { return a.k_magic ? (int)__umulhi((uint32_t)p, a.k_magic) : p; };
+    // Lists of pairs by expert, experts in the order of their first pairs.  Every
+    // CTA has to get the same lists (they index the partials that CTAs join), so
+    // one warp makes them; the code is kept short, as what runs once costs its
+    // instruction fetches.
+    if (warp == 0) {
+        int met = 0;
+#pragma unroll 1
+        for (int p0 = 0; p0 < R; p0 += 32) {
+            const int p = p0 + lane, id = p < R ? s_ids[p] : -1;
+            const unsigned same = __match_any_sync(kFull, id), below = (1u << lane) - 1u;
+            const int before = id >= 0 ? s_cnt[id] : 0, rank = __popc(same & below);
+            const bool lead = id >= 0 && rank == 0;
+            const unsigned fresh = __ballot_sync(kFull, lead && before == 0);
+            if (id >= 0) s_ids[p] = id | ((before + rank) << 10);
+            if (lead) s_cnt[id] = before + __popc(same);
+            if (lead && before == 0) s_met[met + __popc(fresh & below)] = (uint16_t)id;
+            met += __popc(fresh);
+            __syncwarp();
+        }
+        int base = 0;   // pairs (low half) and groups (high half) so far
+#pragma unroll 1
+        for (int x0 = 0; x0 < met; x0 += 32) {
+            const int id = x0 + lane < met ? s_met[x0 + lane] : -1;
+            const int c = id >= 0 ? s_cnt[id] : 0, mine = c | ((c + N - 1) / N << 16);
+            int incl = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(kFull, incl, o);
+                if (lane >= o) incl += y;
+            }
+            const int at = base + incl - mine;
+            if (id >= 0) {
+                const int first = at & 0xFFFF;
+                s_cnt[id] = first;
+#pragma unroll 1
+                for (int i = 0; i < c; i += N)
+                    s_groups[(at >> 16) + i / N] =
+                        (uint32_t)min(N, c - i) | ((uint32_t)(first + i) << 6) | ((uint32_t)id << 16);
+            }
+            base += __shfl_sync(kFull, incl, 31);
+        }
+        // the CTA's shares: lane l < 4 works out plan.cur[l]
+        const int G = base >> 16;
+        const bool down = lane & 2;
+        const Share sh = make_share(down ? CB * G * IB2 : G * IB * CB, ctas);
+        const int unit = down ? G * IB2 : CB, inner = down ? IB2 : IB;
+        Cursor c;
+        c.step = sh.begin(cta + (lane & 1));
+        c.a = c.step / max(1, unit);
+        c.b = c.step - c.a * unit;
+        const int x = down ? c.b : c.a;
+        c.c = x / inner;
+        c.d = x - c.c * inner;
+        if (lane < 4) plan.cur[lane] = c;
+        if (lane == 0) {
+            plan.G = G;
+            plan.up = sh;
+        }
+        if (lane == 2) plan.dn = sh;
+        __syncwarp();
+        asm volatile("bar.arrive 2, %0;" ::"n"(kThreads) : "memory");   // the producer needs no more than that
+    } else {
+        asm volatile("bar.sync 2, %0;" ::"n"(kThreads) : "memory");
+        // a pair's place in the list, and its gate weight as fg8_unpermute_combine
+#pragma unroll 1
+        for (int p = tid - 32; p < R; p += kThreads - 32) {
+            const int v = s_ids[p], t = token_of(p);
+            if (v < 0) continue;
+            s_list[s_cnt[v & 1023] + (v >> 10)] = (uint32_t)p | ((uint32_t)t << 16);
+            float w = s_aff[p];
+            if (a.normalize) {
+                float sum = 0.f;
+#pragma unroll 1
+                for (int j = t * a.k; j < (t + 1) * a.k; ++j)
+                    if (s_ids[j] >= 0) sum = __fadd_rn(sum, s_aff[j]);
+                w = sum != 0.f ? __fdiv_rn(w, sum) : 0.f;
+            }
+            s_w[p] = w;
+        }
+        asm volatile("bar.sync 3, %0;" ::"n"(kThreads - 32) : "memory");
+    }
 
-    const Share up((int64_t)G * IB * CB, ctas), dn((int64_t)CB * G * IB2, ctas);
-    const int64_t u0 = up.begin(cta), u1 = up.begin(cta + 1);
-    const int64_t d0 = dn.begin(cta), d1 = dn.begin(cta + 1);
-    const int64_t unit_dn = (int64_t)G * IB2;    // steps of an output block
+    const int G = plan.G;
+    const Cursor cu = plan.cur[0], cd = plan.cur[2];
+    const int u0 = cu.step, u1 = plan.cur[1].step;
+    const int d0 = cd.step, d1 = plan.cur[3].step;
+    const int unit_dn = G * IB2;    // steps of an output block
+    const int n_up = u1 - u0, n_all = n_up + (d1 - d0);
     auto group_n = [&](uint32_t g) { return (int)(g & 63u); };
     auto group_first = [&](uint32_t g) { return (int)((g >> 6) & 1023u); };
     auto group_e = [&](uint32_t g) { return (int)(g >> 16); };
@@ -318,9 +507,9 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
                 }
             };
             if (u0 < u1) {
-                int cb = (int)(u0 % CB), u = (int)(u0 / CB);
-                int ib = u % IB, g = u / IB;
-                for (int64_t s = u0; s < u1; ++s) {
+                int cb = cu.b, g = cu.c, ib = cu.d;
+#pragma unroll 1
+                for (int s = u0; s < u1; ++s) {
                     if (!(ok = take())) break;
                     const uint32_t dst = sbase + stage * K::kStage;
                     const int row = group_e(s_groups[g]) * 2 * a.I + 128 * ib;
@@ -335,9 +524,9 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
                 }
             }
             if (ok && d0 < d1) {
-                int cb = (int)(d0 / unit_dn), r = (int)(d0 % unit_dn);
-                int g = r / IB2, k2 = r % IB2;
-                for (int64_t s = d0; s < d1; ++s) {
+                int cb = cd.a, g = cd.c, k2 = cd.d;
+#pragma unroll 1
+                for (int s = d0; s < d1; ++s) {
                     if (!(ok = take())) break;
                     const uint32_t dst = sbase + stage * K::kStage;
                     const int row = group_e(s_groups[g]) * a.C + 128 * cb;
@@ -364,9 +553,9 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
             // -------------------------------------------- MMA issuer
             constexpr uint32_t kIdesc = idesc_e4m3(128, N);
             uint32_t stage = 0, phase = 0, buf = 0, bphase = 0;
-            int k2 = d0 < d1 ? (int)(d0 % unit_dn) % IB2 : 0;
-            const int64_t n_up = u1 - u0, n_all = n_up + (d1 - d0);
-            for (int64_t n = 0; n < n_all; ++n) {
+            int k2 = cd.d;
+#pragma unroll 1
+            for (int n = 0; n < n_all; ++n) {
                 if (!mbar_wait(tempty_bar(buf), bphase ^ 1u, abort_flag, a.status) ||
                     !mbar_wait(full_bar(stage), phase, abort_flag, a.status))
                     break;
@@ -405,83 +594,103 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
         }
     } else if (warp >= 8) {
         // ------------------------------------------------ operand B
+        // fill warp w takes the steps n = w, w + 4, ...: the first use of a stage
+        // that is not yet free is at most one phase ahead (4 <= stages)
         const int fw = warp - 8;
         const int half = lane >> 4, hl = lane & 15;
-        const int64_t n_up = u1 - u0, n_all = n_up + (d1 - d0);
-        bool passed = false;   // the grid barrier
-        for (int64_t n = fw; n < n_all; n += kFillWarps) {
-            const uint32_t stage = (uint32_t)(n % S), phase = (uint32_t)(n / S) & 1u;
-            float* f = s_factors + (int)(n % K::kSlots) * 2 * N;
-            uint8_t* B = smem + stage * K::kStage + kABytes;
-            if (n < n_up) {
-                const int64_t s = u0 + n;
-                const int cb = (int)(s % CB), u = (int)(s / CB), ib = u % IB;
-                const uint32_t g = s_groups[u / IB];
-                const int cnt = group_n(g), first = group_first(g);
-                const float* sw = a.sw_up + ((int64_t)group_e(g) * 2 * IB + ib) * CB + cb;
+        uint32_t stage = fw, phase = 0;
+        int slot = fw, n = fw;
+        auto next = [&]() {
+            n += kFillWarps;
+            if ((stage += kFillWarps) >= S) {
+                stage -= S;
+                phase ^= 1u;
+            }
+            if ((slot += kFillWarps) >= K::kSlots) slot -= K::kSlots;
+        };
+        if (n < n_up) {
+            int cb = cu.b + n, g = cu.c, ib = cu.d;
+#pragma unroll 1
+            for (; cb >= CB; cb -= CB)
+                if (++ib == IB) ib = 0, ++g;
+#pragma unroll 1
+            while (n < n_up) {
+                const uint32_t gr = s_groups[g];
+                const int cnt = group_n(gr);
+                const uint32_t* list = s_list + group_first(gr);
+                float* f = s_factors + slot * 2 * N;
+                uint8_t* B = smem + stage * K::kStage + kABytes;
+                const float* sw = a.sw_up + ((int64_t)group_e(gr) * 2 * IB + ib) * CB + cb;
                 const float swg = __ldg(sw), swu = __ldg(sw + (int64_t)IB * CB);
-                uint4 v[N / 2];   // this half-warp's tokens, 8 values a lane
-#pragma unroll
-                for (int i = 0; i < N / 2; ++i) {
-                    const int j = 2 * i + half;
-                    v[i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (j < cnt)
-                        v[i] = __ldg(reinterpret_cast<const uint4*>(a.x + (int64_t)(s_list[first + j] / a.k) * a.C +
-                                                                    128 * cb + 8 * hl));
-                }
+                const uint16_t* xc = a.x + 128 * cb + 8 * hl;
+                // half a warp a token, two tokens of each half ahead
+                auto load = [&](int j) {
+                    return j < cnt ? __ldg(reinterpret_cast<const uint4*>(xc + (int64_t)(list[j] >> 16) * a.C))
+                                   : make_uint4(0u, 0u, 0u, 0u);
+                };
+                uint4 v0 = load(half), v1 = load(2 + half);
                 if (!(ok = mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, a.status))) break;
+#pragma unroll 1
+                for (int j0 = 0; j0 < cnt; j0 += 2) {
+                    const uint4 v = v0;
+                    const int j = j0 + half;
+                    v0 = v1;
+                    v1 = load(j + 4);
+                    float m = fg8::amax8(v);
 #pragma unroll
-                for (int i = 0; i < N / 2; ++i) {
-                    if (2 * i < cnt) {   // warp-uniform
-                        const int j = 2 * i + half;
-                        float m = fg8::amax8(v[i]);
-#pragma unroll
-                        for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-                        const float sc = fg8::tile_scale(m);
-                        const uint2 q = fg8::quant8(v[i], fg8::make_qscale(sc));
-                        *reinterpret_cast<uint2*>(B + j * 128 + (((hl >> 1) ^ (j & 7)) << 4) + 8 * (hl & 1)) = q;
-                        if (hl == 0) {
-                            f[j] = sc * swg;
-                            f[N + j] = sc * swu;
-                        }
+                    for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+                    const float sc = fg8::tile_scale_fast(m);
+                    *reinterpret_cast<uint2*>(B + j * 128 + (((hl >> 1) ^ (j & 7)) << 4) + 8 * (hl & 1)) =
+                        quant8_corrected(v, sc);
+                    if (hl == 0) {
+                        f[j] = sc * swg;
+                        f[N + j] = sc * swu;
                     }
                 }
-            } else {
-                if (!passed) {
-                    // all of h is written once every CTA has arrived
-                    if (lane == 0) {
-                        const uint64_t t0 = fg8::globaltimer_ns();
-                        while (fg8::ld_acquire_gpu(&a.head->bar_gen) == *s_gen) {
-                            if (*abort_flag) break;
-                            if (fg8::globaltimer_ns() - t0 > fg8::kWaitLimitNs) {
-                                fg8::set_status(a.status, FG8_ERR_TIMEOUT);
-                                *abort_flag = 1;
-                                break;
-                            }
-                        }
-                        __threadfence();
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full_bar(stage));
+                next();
+#pragma unroll 1
+                for (cb += kFillWarps; cb >= CB; cb -= CB)
+                    if (++ib == IB) ib = 0, ++g;
+            }
+        }
+        if (ok && fw == 0 && d0 < d1) {
+            // all of h is written once every CTA has arrived; one poller a CTA
+            if (lane == 0) {
+                const uint32_t all = *s_call * (uint32_t)ctas;
+                const uint64_t t0 = fg8::globaltimer_ns();
+                while ((int32_t)(fg8::ld_acquire_gpu(&a.head->h_done) - all) < 0 && !*abort_flag) {
+                    if (fg8::globaltimer_ns() - t0 > fg8::kWaitLimitNs) {
+                        fg8::set_status(a.status, FG8_ERR_TIMEOUT);
+                        *abort_flag = 1;
                     }
-                    __syncwarp();
-                    if (*abort_flag) {
-                        ok = false;
-                        break;
-                    }
-                    passed = true;
                 }
-                const int64_t s = d0 + (n - n_up);
-                const int cb = (int)(s / unit_dn), r = (int)(s % unit_dn), k2 = r % IB2;
-                const uint32_t g = s_groups[r / IB2];
-                const int cnt = group_n(g), first = group_first(g);
+                mbar_arrive(h_bar);
+            }
+            __syncwarp();
+        }
+        if (ok && n < n_all && (ok = mbar_wait(h_bar, 0, abort_flag, a.status))) {
+            int cb = cd.a, g = cd.c, k2 = cd.d + n - n_up;
+#pragma unroll 1
+            for (; k2 >= IB2; k2 -= IB2)
+                if (++g == G) g = 0, ++cb;
+#pragma unroll 1
+            while (n < n_all && !*abort_flag) {
+                const uint32_t gr = s_groups[g];
+                const int cnt = group_n(gr);
+                const uint32_t* list = s_list + group_first(gr);
+                float* f = s_factors + slot * 2 * N;
+                uint8_t* B = smem + stage * K::kStage + kABytes + (hl >> 3) * N * 128;
                 const bool mine = 2 * k2 + (hl >> 3) < IB;   // this lane's K block exists
-                uint4 v[N / 2];
-#pragma unroll
-                for (int i = 0; i < N / 2; ++i) {
-                    const int j = 2 * i + half;
-                    v[i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (j < cnt && mine)
-                        v[i] = __ldcg(reinterpret_cast<const uint4*>(a.hq + (int64_t)s_list[first + j] * a.I +
-                                                                     256 * k2 + 16 * hl));
-                }
+                const uint8_t* hc = a.hq + 256 * k2 + 16 * hl;
+                auto load = [&](int j) {   // half a warp a pair: 128 codes of each of the two K blocks
+                    return j < cnt && mine
+                               ? __ldcg(reinterpret_cast<const uint4*>(hc + (int64_t)(list[j] & 0xFFFFu) * a.I))
+                               : make_uint4(0u, 0u, 0u, 0u);
+                };
+                uint4 v0 = load(half), v1 = load(2 + half);
                 // factors: lane = token of the first block, then of the second
                 float fac[2 * N / 32];
 #pragma unroll
@@ -489,24 +698,30 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
                     const int idx = 32 * i + lane, j = idx % N, kb = 2 * k2 + idx / N;
                     fac[i] = 0.f;
                     if (j < cnt && kb < IB) {
-                        const int p = s_list[first + j];
+                        const int p = list[j] & 0xFFFFu;
                         fac[i] = __ldcg(a.sh + (int64_t)p * IB + kb) *
-                                 __ldg(a.sw_dn + ((int64_t)group_e(g) * CB + cb) * IB + kb) * s_w[p];
+                                 __ldg(a.sw_dn + ((int64_t)group_e(gr) * CB + cb) * IB + kb) * s_w[p];
                     }
                 }
                 if (!(ok = mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, a.status))) break;
-#pragma unroll
-                for (int i = 0; i < N / 2; ++i) {
-                    const int j = 2 * i + half;
-                    if (j < cnt)
-                        *reinterpret_cast<uint4*>(B + (hl >> 3) * N * 128 + j * 128 + (((hl & 7) ^ (j & 7)) << 4)) = v[i];
+#pragma unroll 1
+                for (int j0 = 0; j0 < cnt; j0 += 2) {
+                    const uint4 v = v0;
+                    const int j = j0 + half;
+                    v0 = v1;
+                    v1 = load(j + 4);
+                    *reinterpret_cast<uint4*>(B + j * 128 + (((hl & 7) ^ (j & 7)) << 4)) = v;
                 }
 #pragma unroll
                 for (int i = 0; i < 2 * N / 32; ++i) f[32 * i + lane] = fac[i];
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full_bar(stage));
+                next();
+#pragma unroll 1
+                for (k2 += kFillWarps; k2 >= IB2; k2 -= IB2)
+                    if (++g == G) g = 0, ++cb;
             }
-            fence_async_shared();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(full_bar(stage));
         }
     } else if (warp >= 4) {
         // ------------------------------------------------ promotion
@@ -556,25 +771,35 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
             return true;
         };
         // where CTA c keeps its partial of a unit that begins at step `begin`
-        auto part_of = [&](int c, const Share& sh, int64_t begin) {
+        auto part_of = [&](int c, const Share& sh, int begin) {
             return a.part + (int64_t)(2 * c + (begin > sh.begin(c) ? 1 : 0)) * a.part_floats;
         };
 
-        // ---- up-projection
-        if (u0 < u1) {
-            int cb = (int)(u0 % CB), u = (int)(u0 / CB);
+        float* my_acc = s_acc + row;   // this thread's column, its alone
+        auto clear = [&]() {
 #pragma unroll
             for (int i = 0; i < 2 * N; ++i) acc[i] = 0.f;
-            for (int64_t s = u0; ok && s < u1; ++s) {
+        };
+        // ---- up-projection
+        if (u0 < u1) {
+            const Share up = plan.up;
+            int u = cu.a, cb = cu.b;
+            clear();
+#pragma unroll 1
+            for (int s = u0; s < u1; ++s) {
                 if (!(ok = promote(true))) break;
                 if (++cb < CB && s + 1 < u1) continue;
                 // this CTA's part of unit u is done
-                const int ib = u % IB;
-                const uint32_t g = s_groups[u / IB];
-                const int cnt = group_n(g), first = group_first(g);
-                const int64_t ub = (int64_t)u * CB, ue = ub + CB;
+                const int g = u / IB, ib = u - g * IB;
+                const uint32_t gr = s_groups[g];
+                const int cnt = group_n(gr);
+                const uint32_t* list = s_list + group_first(gr);
+                const int ub = u * CB, ue = ub + CB;
                 bool finish = true;
-                if (ub < u0 || ue > u1) {
+                if (ub >= u0 && ue <= u1) {
+#pragma unroll
+                    for (int i = 0; i < 2 * N; ++i) my_acc[i * 128] = acc[i];
+                } else {
                     float* my = part_of(cta, up, ub) + row;
 #pragma unroll
                     for (int j = 0; j < N; ++j)
@@ -582,7 +807,6 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
                             __stcg(my + j * 128, acc[j]);
                             __stcg(my + (N + j) * 128, acc[N + j]);
                         }
-                    __threadfence();
                     if (!(ok = meet())) break;
                     const int c0 = up.owner(ub), c1 = up.owner(ue - 1);
                     if (warp == 4 && lane == 0) {
@@ -596,16 +820,17 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
                     finish = s_last[joint & 1u] != 0;
                     if (finish) {
                         __threadfence();
-#pragma unroll
-                        for (int i = 0; i < 2 * N; ++i) acc[i] = 0.f;
-                        for (int c = c0; c <= c1; ++c) {
-                            const float* pp = part_of(c, up, ub) + row;
-#pragma unroll
-                            for (int j = 0; j < N; ++j)
-                                if (j < cnt) {
-                                    acc[j] += __ldcg(pp + j * 128);
-                                    acc[N + j] += __ldcg(pp + (N + j) * 128);
-                                }
+#pragma unroll 2
+                        for (int j = 0; j < cnt; ++j) {
+                            float sg = 0.f, su = 0.f;
+#pragma unroll 4
+                            for (int c = c0; c <= c1; ++c) {
+                                const float* pp = part_of(c, up, ub) + j * 128 + row;
+                                sg += __ldcg(pp);
+                                su += __ldcg(pp + N * 128);
+                            }
+                            my_acc[j * 128] = sg;
+                            my_acc[(N + j) * 128] = su;
                         }
                     }
                 }
@@ -613,44 +838,33 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
                     // h = silu(gate) up for this row's column of every token, one
                     // 1x128 tile a token over the 128 threads
                     float* red = s_red + (joint & 1u) * 4 * N;
-#pragma unroll
-                    for (int j = 0; j < N; ++j)
-                        if (j < cnt) {
-                            acc[j] = silu_mul(acc[j], acc[N + j]);
-                            const uint32_t m = __reduce_max_sync(kFull, __float_as_uint(fabsf(acc[j])));
-                            if (lane == 0) red[quarter * N + j] = __uint_as_float(m);
-                        }
+#pragma unroll 2
+                    for (int j = 0; j < cnt; ++j) {
+                        const float h = silu_mul(my_acc[j * 128], my_acc[(N + j) * 128]);
+                        my_acc[j * 128] = h;
+                        const uint32_t m = __reduce_max_sync(kFull, __float_as_uint(fabsf(h)));
+                        if (lane == 0) red[quarter * N + j] = __uint_as_float(m);
+                    }
                     if (!(ok = meet())) break;
-#pragma unroll
-                    for (int j = 0; j < N; ++j)
-                        if (j < cnt) {
-                            const float m = fmaxf(fmaxf(red[j], red[N + j]), fmaxf(red[2 * N + j], red[3 * N + j]));
-                            const float sc = fg8::tile_scale32(m);
-                            const int p = s_list[first + j];
-                            a.hq[(int64_t)p * a.I + 128 * ib + row] =
-                                (uint8_t)fg8::cvt_e4m3x2(__fdiv_rn(acc[j], sc), 0.f);
-                            if (row == 0) a.sh[(int64_t)p * IB + ib] = sc;
-                        }
+#pragma unroll 2
+                    for (int j = 0; j < cnt; ++j) {
+                        const float m = fmaxf(fmaxf(red[j], red[N + j]), fmaxf(red[2 * N + j], red[3 * N + j]));
+                        const float sc = fg8::tile_scale_fast(m);
+                        const int p = list[j] & 0xFFFFu;
+                        a.hq[(int64_t)p * a.I + 128 * ib + row] = (uint8_t)code_of(my_acc[j * 128], sc);
+                        if (row == 0) a.sh[(int64_t)p * IB + ib] = sc;
+                    }
                 }
                 ++joint;
                 cb = 0;
                 ++u;
-#pragma unroll
-                for (int i = 0; i < 2 * N; ++i) acc[i] = 0.f;
+                clear();
             }
         }
         // ---- grid barrier: this CTA's h is written
-        if (ok) {
-            __threadfence();
-            if ((ok = meet()) && warp == 4 && lane == 0) {
-                __threadfence();
-                const uint32_t old = atomicInc(&a.head->bar_count, (uint32_t)ctas - 1u);
-                if (old > (uint32_t)ctas - 1u) fg8::set_status(a.status, FG8_ERR_WORKSPACE_SHARED);
-                if (old == (uint32_t)ctas - 1u) {
-                    __threadfence();
-                    atomicAdd(&a.head->bar_gen, 1u);
-                }
-            }
+        if (ok && (ok = meet()) && warp == 4 && lane == 0) {
+            a.head->calls[cta] = *s_call;
+            red_release_gpu(&a.head->h_done, 1u);
         }
         // ---- down-projection
         auto store_out = [&](int t, int c, float v) {
@@ -658,73 +872,77 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
             else static_cast<uint16_t*>(a.out)[(int64_t)t * a.C + c] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
         };
         if (ok && d0 < d1) {
-            int cb = (int)(d0 / unit_dn), r = (int)(d0 % unit_dn);
-            int g = r / IB2, k2 = r % IB2;
-            for (int t = 0; t < a.T; ++t) s_acc[t * 128 + row] = 0.f;   // this thread's column, its alone
-#pragma unroll
-            for (int i = 0; i < 2 * N; ++i) acc[i] = 0.f;
-            for (int64_t s = d0; ok && s < d1; ++s) {
+            const Share dn = plan.dn;
+            int cb = cd.a, g = cd.c, k2 = cd.d;
+#pragma unroll 1
+            for (int t = 0; t < a.T; ++t) my_acc[t * 128] = 0.f;
+            clear();
+#pragma unroll 1
+            for (int s = d0; s < d1; ++s) {
                 if (!(ok = promote(2 * k2 + 1 < IB))) break;
                 const bool cut = s + 1 == d1;
                 if (++k2 < IB2 && !cut) continue;
                 k2 = 0;
                 // the group's (or this CTA's last) columns into their tokens' sums
                 const uint32_t gr = s_groups[g];
-                const int cnt = group_n(gr), first = group_first(gr);
+                const int cnt = group_n(gr);
+                const uint32_t* list = s_list + group_first(gr);
 #pragma unroll
                 for (int j = 0; j < N; ++j)
-                    if (j < cnt) {
-                        float* o = s_acc + (s_list[first + j] / a.k) * 128 + row;
-                        *o += acc[j] + acc[N + j];
-                    }
-#pragma unroll
-                for (int i = 0; i < 2 * N; ++i) acc[i] = 0.f;
+                    if (j < cnt) my_acc[(list[j] >> 16) * 128] += acc[j] + acc[N + j];
+                clear();
                 if (++g < G && !cut) continue;
                 g = 0;
                 // this CTA's part of output block cb is done
-                const int64_t ub = (int64_t)cb * unit_dn, ue = ub + unit_dn;
+                const int ub = cb * unit_dn, ue = ub + unit_dn;
                 if (ub >= d0 && ue <= d1) {
-                    for (int t = 0; t < a.T; ++t) store_out(t, 128 * cb + row, s_acc[t * 128 + row]);
+#pragma unroll 1
+                    for (int t = 0; t < a.T; ++t) store_out(t, 128 * cb + row, my_acc[t * 128]);
                 } else {
                     float* my = part_of(cta, dn, ub) + row;
-                    for (int t = 0; t < a.T; ++t) __stcg(my + t * 128, s_acc[t * 128 + row]);
-                    __threadfence();
+#pragma unroll 4
+                    for (int t = 0; t < a.T; ++t) __stcg(my + t * 128, my_acc[t * 128]);
                     if (!(ok = meet())) break;
-                    if (warp == 4 && lane == 0) {
-                        __threadfence();
-                        atomicAdd(&a.head->down_count[dn.owner(ub)], 1u);
-                    }
+                    if (warp == 4 && lane == 0) st_release_gpu(&a.head->part_done[cta][ub > d0], *s_call);
                 }
-                for (int t = 0; t < a.T; ++t) s_acc[t * 128 + row] = 0.f;
+#pragma unroll 1
+                for (int t = 0; t < a.T; ++t) my_acc[t * 128] = 0.f;
                 ++cb;
             }
             // cut blocks (at most the first and the last of this CTA's): once all
-            // their parts are there, each of their CTAs joins its share of the tokens
-            const int cb0 = (int)(d0 / unit_dn), cb1 = (int)((d1 - 1) / unit_dn);
-            for (int w = 0; ok && w < 2; ++w) {
-                const int c = w == 0 ? cb0 : cb1;
-                if (w == 1 && cb1 == cb0) break;
-                const int64_t ub = (int64_t)c * unit_dn, ue = ub + unit_dn;
+            // their parts are there, each of their CTAs joins its share of the
+            // T x 128 sums, four columns a thread
+            const int cb0 = cd.a, cb1 = plan.cur[3].b ? plan.cur[3].a : plan.cur[3].a - 1;
+#pragma unroll 1
+            for (int c = cb0; ok && c <= cb1; c += max(1, cb1 - cb0)) {
+                const int ub = c * unit_dn, ue = ub + unit_dn;
                 if (ub >= d0 && ue <= d1) continue;
                 const int c0 = dn.owner(ub), c1 = dn.owner(ue - 1), n = c1 - c0 + 1;
-                if (warp == 4 && lane == 0) {
-                    const uint64_t t0 = fg8::globaltimer_ns();
-                    while (fg8::ld_acquire_gpu(&a.head->down_count[c0]) < (uint32_t)n) {
-                        if (*abort_flag) break;
-                        if (fg8::globaltimer_ns() - t0 > fg8::kWaitLimitNs) {
-                            fg8::set_status(a.status, FG8_ERR_TIMEOUT);
-                            *abort_flag = 1;
-                            break;
-                        }
-                    }
-                    __threadfence();
+                // the block begins inside the first CTA's share (its later part) or
+                // with it; for all others it is their first
+                if (warp == 4) {
+                    const uint32_t* first = &a.head->part_done[c0][ub > dn.begin(c0)];
+                    wait_calls(first, 2, 1, *s_call, lane, abort_flag, a.status);
+                    wait_calls(&a.head->part_done[c0 + 1][0], 2, n - 1, *s_call, lane, abort_flag, a.status);
                 }
                 if (!(ok = meet()) || *abort_flag) break;
-                const int t1 = a.T * (cta - c0 + 1) / n;
-                for (int t = a.T * (cta - c0) / n; t < t1; ++t) {
-                    float v = 0.f;
-                    for (int q = c0; q <= c1; ++q) v += __ldcg(part_of(q, dn, ub) + t * 128 + row);
-                    store_out(t, 128 * c + row, v);
+                const int quads = 32 * a.T, q1 = quads * (cta - c0 + 1) / n;
+#pragma unroll 1
+                for (int q = quads * (cta - c0) / n + row; q < q1; q += 128) {
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+                    for (int w = c0; w <= c1; ++w) {
+                        const float4 pv = __ldcg(reinterpret_cast<const float4*>(part_of(w, dn, ub)) + q);
+                        v.x += pv.x;
+                        v.y += pv.y;
+                        v.z += pv.z;
+                        v.w += pv.w;
+                    }
+                    const int t = q >> 5, col = 128 * c + 4 * (q & 31);
+                    store_out(t, col, v.x);
+                    store_out(t, col + 1, v.y);
+                    store_out(t, col + 2, v.z);
+                    store_out(t, col + 3, v.w);
                 }
             }
         }
@@ -795,6 +1013,7 @@ extern "C" fg8_status fg8_moe_decode(const uint16_t* x, int64_t T, int C, const 
     if (out_dtype != FG8_OUT_BF16 && out_dtype != FG8_OUT_F32) return FG8_ERR_INVALID_ARG;
     if (T > kMaxT || k > fg8::kRouteMaxK || E > kMaxE) return FG8_ERR_UNSUPPORTED;
     if ((int64_t)E * 2 * I > INT32_MAX || (int64_t)E * C > INT32_MAX) return FG8_ERR_UNSUPPORTED;
+    if ((T * k) * (int64_t)(I / 128) * (C / 128) > INT32_MAX) return FG8_ERR_UNSUPPORTED;   // steps
     if (T == 0) return FG8_OK;
     if (!x || !topk_ids || !affinity || !wq_up || !sw_up || !wq_dn || !sw_dn || !out || !workspace ||
         (logits && !bias))
@@ -818,6 +1037,7 @@ extern "C" fg8_status fg8_moe_decode(const uint16_t* x, int64_t T, int C, const 
     a.x = x; a.logits = logits; a.bias = bias; a.ids = topk_ids; a.affinity = affinity;
     a.sw_up = sw_up; a.sw_dn = sw_dn;
     a.T = (int)T; a.k = k; a.E = E; a.C = C; a.I = I;
+    a.k_magic = k == 1 ? 0u : (uint32_t)(((1ull << 32) + k - 1) / k);
     a.normalize = normalize; a.out_f32 = out_dtype == FG8_OUT_F32; a.out = out;
     a.head = reinterpret_cast<Head*>(ws);
     a.hq = ws + l.hq;

@@ -199,8 +199,6 @@ def test_equal_calls_equal_bits_on_one_workspace_of_many_sizes():
         if first is None:
             first = oa.clone(), ob.clone()
         assert torch.equal(oa, first[0]) and torch.equal(ob, first[1])
-    head = ws[:fg8.FG8_MOE_DECODE_HEAD].view(torch.int32)
-    assert head[0].item() == 0 and torch.all(head[16:16 + 160] == 0)
 
 
 def test_close_to_the_chain_of_kernels():
