@@ -26,14 +26,19 @@
 // the down-projection: two K blocks of 128 output columns.  A unit is what ends in
 // one result: (group, 128 columns of h), then 128 columns of out over all experts.
 // A unit cut between CTAs is joined from fp32 partials in the caller's workspace,
-// always in CTA order, so results do not vary between runs: for h the last CTA
-// to arrive joins (it needs the column maxima); for out, whose partials hold all
-// T tokens, every CTA that has a part joins its share of the rows.
+// always in CTA order, so results do not vary between runs.  A unit of h is joined
+// by its first CTA: the others meet it at the beginning of their shares, so their
+// parts are there long before the first one's, the end of its share.  For out,
+// whose partials hold all T tokens, every CTA that has a part joins its share of
+// the T x 128 sums.
+//
+// x is quantized once, a tile a half-warp over all CTAs (the bits of
+// fg8_quantize_act), while the routing is worked out; the meeting that this takes
+// hides behind the first weights' way.
 //
 // Warps: 0 TMA producer, 1 MMA issuer, 4..7 promotion (thread = one weight row:
 // acc[token] += partial * (activation scale * block scale), fp32), 8..11 fill
-// operand B: half a warp quantizes a token's 128 values of x (the bits of
-// fg8_quantize_act), or copies 128 codes of h.
+// operand B (codes of x or h) and the scale products.
 //
 // Every wait is bounded (FG8_ERR_TIMEOUT in *status; the roles wind down and TMEM
 // is released).
@@ -111,8 +116,8 @@ struct Cfg {
     static constexpr uint32_t kOffFactors = kOffAcc + kAccRows * 512;
     static constexpr uint32_t kOffRed = kOffFactors + kSlots * 2 * N * 4;   // float [2][4][N]
     static constexpr uint32_t kOffBars = kOffRed + 2 * 4 * N * 4;
-    static constexpr int kNumBars = 2 * kStages + 2 * kTmemBufs + 3;    // full, empty, tfull, tempty, drain, group, h
-    static constexpr uint32_t kOffMisc = kOffBars + 8 * kNumBars;           // tmem slot, abort, call number, last[2]
+    static constexpr int kNumBars = 2 * kStages + 2 * kTmemBufs + 4;    // full, empty, tfull, tempty, drain, group, x, h
+    static constexpr uint32_t kOffMisc = kOffBars + 8 * kNumBars;           // tmem slot, abort, call number
     static constexpr uint32_t kOffPlan = kOffMisc + 32;
     static constexpr uint32_t kOffGroups = kOffPlan + 128;        // uint32 [kPairs]: n | first << 6 | expert << 16
     static constexpr uint32_t kOffList = kOffGroups + 4 * kPairs;   // uint32 [kPairs]: pair | token << 16, experts ascending
@@ -127,17 +132,17 @@ struct Cfg {
     static_assert(sizeof(Plan) <= 128, "plan");
 };
 
-// workspace: a fixed head of counters (zero between calls), then h, its scales
-// and the partials of cut units
+// workspace: a fixed head of counters (zero between calls), then the codes
+// and scales of x and h and the partials of cut units
 constexpr size_t kHeadBytes = FG8_MOE_DECODE_HEAD;
 struct Head {
-    // call numbers order the arrivals, so nothing is cleared between calls: a
-    // CTA's h is written (the grid barrier); its part of the output block that it
-    // shares with earlier [0] or later [1] CTAs is written
-    uint32_t h_done;                 // all CTAs' arrivals of all calls
+    // call numbers order the arrivals, so nothing is cleared between calls;
+    // part_done: its part of the output block that it shares with earlier [0] or
+    // later [1] CTAs is written
+    uint32_t x_done, h_done;         // all CTAs' arrivals of all calls: codes of x, h are written
     uint32_t calls[kMaxCtas];        // calls that the CTA has finished
     uint32_t part_done[kMaxCtas][2];
-    uint32_t up_count[kMaxCtas];     // by the unit's first CTA; 0 between calls
+    uint32_t up_done[kMaxCtas];      // its part of a unit of h that began before its share
 };
 static_assert(sizeof(Head) <= kHeadBytes, "counter head");
 
@@ -154,6 +159,8 @@ struct Args {
     int normalize, out_f32;
     void* out;
     Head* head;
+    uint8_t* xq;             // [T][C]
+    float* sx;               // [T][C / 128]
     uint8_t* hq;             // [T k][I]
     float* sh;               // [T k][I / 128]
     float* part;             // [2 CTAs][part_floats]
@@ -330,11 +337,10 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
     auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * S + b); };
     auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * S + kTmemBufs + b); };
     const uint32_t drain_bar = bar0 + 8u * (2 * S + 2 * kTmemBufs);
-    const uint32_t group_bar = drain_bar + 8u, h_bar = drain_bar + 16u;
+    const uint32_t group_bar = drain_bar + 8u, x_bar = drain_bar + 16u, h_bar = drain_bar + 24u;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + K::kOffMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + K::kOffMisc + 4);
     volatile uint32_t* s_call = reinterpret_cast<volatile uint32_t*>(smem + K::kOffMisc + 8);
-    volatile int* s_last = reinterpret_cast<volatile int*>(smem + K::kOffMisc + 16);   // [2]
     uint32_t* s_groups = reinterpret_cast<uint32_t*>(smem + K::kOffGroups);
     uint32_t* s_list = reinterpret_cast<uint32_t*>(smem + K::kOffList);
     float* s_w = reinterpret_cast<float*>(smem + K::kOffW);
@@ -365,6 +371,7 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
         }
         mbar_init(drain_bar, 1);
         mbar_init(group_bar, 4);
+        mbar_init(x_bar, 1);
         mbar_init(h_bar, 1);
         *abort_flag = 0;
         *s_call = a.head->calls[cta] + 1u;
@@ -379,6 +386,26 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
     if (tid == 96) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_up)) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_dn)) : "memory");
+    }
+    if (warp >= 4) {
+        // tile i of x goes to CTA i mod ctas, half a warp a tile
+        const int hl = lane & 15;
+#pragma unroll 1
+        for (int i = cta + ctas * (2 * (warp - 4) + (lane >> 4)), n = a.T * CB; i - ctas * (lane >> 4) < n; i += 16 * ctas) {
+            // (uniform over the warp: the second half may be past the end)
+            const bool in = i < n;
+            const int64_t at = (int64_t)i * 128 + 8 * hl;   // tile i = token i / CB, block i % CB: contiguous in x
+            const uint4 v = in ? __ldg(reinterpret_cast<const uint4*>(a.x + at)) : make_uint4(0u, 0u, 0u, 0u);
+            float m = fg8::amax8(v);
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+            const float sc = fg8::tile_scale_fast(m);
+            const uint2 q = quant8_corrected(v, sc);
+            if (in) {
+                *reinterpret_cast<uint2*>(a.xq + at) = q;
+                if (hl == 0) a.sx[i] = sc;
+            }
+        }
     }
     if (a.logits) {
         // warp 0 has no other set-up: with one token it starts on it at once
@@ -401,6 +428,7 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
+    if (tid == kThreads - 1) red_release_gpu(&a.head->x_done, 1u);
     auto token_of = [&](int p) { return a.k_magic ? (int)__umulhi((uint32_t)p, a.k_magic) : p; };
     // Lists of pairs by expert, experts in the order of their first pairs.  Every
     // CTA has to get the same lists (they index the partials that CTAs join), so
@@ -597,7 +625,7 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
         // fill warp w takes the steps n = w, w + 4, ...: the first use of a stage
         // that is not yet free is at most one phase ahead (4 <= stages)
         const int fw = warp - 8;
-        const int half = lane >> 4, hl = lane & 15;
+        const int sub = lane >> 3, ch = lane & 7;   // a row's 128 codes: 8 lanes
         uint32_t stage = fw, phase = 0;
         int slot = fw, n = fw;
         auto next = [&]() {
@@ -608,119 +636,126 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
             }
             if ((slot += kFillWarps) >= K::kSlots) slot -= K::kSlots;
         };
-        if (n < n_up) {
-            int cb = cu.b + n, g = cu.c, ib = cu.d;
-#pragma unroll 1
-            for (; cb >= CB; cb -= CB)
-                if (++ib == IB) ib = 0, ++g;
-#pragma unroll 1
-            while (n < n_up) {
-                const uint32_t gr = s_groups[g];
-                const int cnt = group_n(gr);
-                const uint32_t* list = s_list + group_first(gr);
-                float* f = s_factors + slot * 2 * N;
-                uint8_t* B = smem + stage * K::kStage + kABytes;
-                const float* sw = a.sw_up + ((int64_t)group_e(gr) * 2 * IB + ib) * CB + cb;
-                const float swg = __ldg(sw), swu = __ldg(sw + (int64_t)IB * CB);
-                const uint16_t* xc = a.x + 128 * cb + 8 * hl;
-                // half a warp a token, two tokens of each half ahead
-                auto load = [&](int j) {
-                    return j < cnt ? __ldg(reinterpret_cast<const uint4*>(xc + (int64_t)(list[j] >> 16) * a.C))
-                                   : make_uint4(0u, 0u, 0u, 0u);
-                };
-                uint4 v0 = load(half), v1 = load(2 + half);
-                if (!(ok = mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, a.status))) break;
-#pragma unroll 1
-                for (int j0 = 0; j0 < cnt; j0 += 2) {
-                    const uint4 v = v0;
-                    const int j = j0 + half;
-                    v0 = v1;
-                    v1 = load(j + 4);
-                    float m = fg8::amax8(v);
-#pragma unroll
-                    for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-                    const float sc = fg8::tile_scale_fast(m);
-                    *reinterpret_cast<uint2*>(B + j * 128 + (((hl >> 1) ^ (j & 7)) << 4) + 8 * (hl & 1)) =
-                        quant8_corrected(v, sc);
-                    if (hl == 0) {
-                        f[j] = sc * swg;
-                        f[N + j] = sc * swu;
-                    }
-                }
-                fence_async_shared();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(full_bar(stage));
-                next();
-#pragma unroll 1
-                for (cb += kFillWarps; cb >= CB; cb -= CB)
-                    if (++ib == IB) ib = 0, ++g;
-            }
-        }
-        if (ok && fw == 0 && d0 < d1) {
-            // all of h is written once every CTA has arrived; one poller a CTA
-            if (lane == 0) {
+        // all CTAs have written what this one reads next: fill warp 0 watches, the
+        // others wait for it here
+        auto wait_all = [&](const uint32_t* arrivals, uint32_t bar) {
+            if (fw == 0 && lane == 0) {
                 const uint32_t all = *s_call * (uint32_t)ctas;
                 const uint64_t t0 = fg8::globaltimer_ns();
-                while ((int32_t)(fg8::ld_acquire_gpu(&a.head->h_done) - all) < 0 && !*abort_flag) {
+                while ((int32_t)(fg8::ld_acquire_gpu(arrivals) - all) < 0 && !*abort_flag) {
                     if (fg8::globaltimer_ns() - t0 > fg8::kWaitLimitNs) {
                         fg8::set_status(a.status, FG8_ERR_TIMEOUT);
                         *abort_flag = 1;
                     }
                 }
-                mbar_arrive(h_bar);
+                mbar_arrive(bar);
             }
             __syncwarp();
-        }
-        if (ok && n < n_all && (ok = mbar_wait(h_bar, 0, abort_flag, a.status))) {
-            int cb = cd.a, g = cd.c, k2 = cd.d + n - n_up;
+            return mbar_wait(bar, 0, abort_flag, a.status) && !*abort_flag;
+        };
+        // rows of 128 codes, row j at base + stride * index(j): all loads, then,
+        // once the stage is free, all stores
+        auto load_rows = [&](uint4 (&v)[N / 4], const uint8_t* base, int stride, const uint32_t* list, int shift, int cnt) {
+#pragma unroll
+            for (int i = 0; i < N / 4; ++i)
+                if (4 * i < cnt) {   // warp-uniform
+                    const int j = min(4 * i + sub, cnt - 1);
+                    v[i] = __ldcg(reinterpret_cast<const uint4*>(base + (int64_t)((list[j] >> shift) & 0xFFFFu) * stride + 16 * ch));
+                }
+        };
+        auto store_rows = [&](const uint4 (&v)[N / 4], uint8_t* B, int cnt) {
+#pragma unroll
+            for (int i = 0; i < N / 4; ++i)
+                if (4 * i < cnt) {
+                    const int j = 4 * i + sub;   // rows past cnt, < N, repeat the last: their columns are not used
+                    *reinterpret_cast<uint4*>(B + j * 128 + ((ch ^ (j & 7)) << 4)) = v[i];
+                }
+        };
+        // this lane's factors: index 32 i + lane is token index % N of the first
+        // (gate / first block) or second (up / second block) product
+        constexpr int F = 2 * N / 32;
+        auto publish = [&](const float (&fac)[F]) {
+            float* f = s_factors + slot * 2 * N;
+#pragma unroll
+            for (int i = 0; i < F; ++i) f[32 * i + lane] = fac[i];
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full_bar(stage));
+        };
+        ok = n_all == 0 || wait_all(&a.head->x_done, x_bar);
+        if (ok && n < n_up) {
+            int cb = cu.b + n, g = cu.c, ib = cu.d;
+            // block scales of a step, loaded a step ahead (they come from HBM)
+            float sw[F];
+            auto advance = [&]() {
 #pragma unroll 1
-            for (; k2 >= IB2; k2 -= IB2)
-                if (++g == G) g = 0, ++cb;
+                for (; cb >= CB; cb -= CB)
+                    if (++ib == IB) ib = 0, ++g;
+#pragma unroll
+                for (int i = 0; i < F; ++i)
+                    sw[i] = __ldg(a.sw_up + ((int64_t)group_e(s_groups[g]) * 2 * IB + ib + (32 * i + lane) / N * IB) * CB + cb);
+            };
+            advance();
 #pragma unroll 1
-            while (n < n_all && !*abort_flag) {
+            while (n < n_up) {
                 const uint32_t gr = s_groups[g];
                 const int cnt = group_n(gr);
                 const uint32_t* list = s_list + group_first(gr);
-                float* f = s_factors + slot * 2 * N;
-                uint8_t* B = smem + stage * K::kStage + kABytes + (hl >> 3) * N * 128;
-                const bool mine = 2 * k2 + (hl >> 3) < IB;   // this lane's K block exists
-                const uint8_t* hc = a.hq + 256 * k2 + 16 * hl;
-                auto load = [&](int j) {   // half a warp a pair: 128 codes of each of the two K blocks
-                    return j < cnt && mine
-                               ? __ldcg(reinterpret_cast<const uint4*>(hc + (int64_t)(list[j] & 0xFFFFu) * a.I))
-                               : make_uint4(0u, 0u, 0u, 0u);
-                };
-                uint4 v0 = load(half), v1 = load(2 + half);
-                // factors: lane = token of the first block, then of the second
-                float fac[2 * N / 32];
+                uint4 v[N / 4];
+                load_rows(v, a.xq + 128 * cb, a.C, list, 16, cnt);
+                float fac[F];
 #pragma unroll
-                for (int i = 0; i < 2 * N / 32; ++i) {
-                    const int idx = 32 * i + lane, j = idx % N, kb = 2 * k2 + idx / N;
-                    fac[i] = 0.f;
-                    if (j < cnt && kb < IB) {
-                        const int p = list[j] & 0xFFFFu;
-                        fac[i] = __ldcg(a.sh + (int64_t)p * IB + kb) *
-                                 __ldg(a.sw_dn + ((int64_t)group_e(gr) * CB + cb) * IB + kb) * s_w[p];
-                    }
+                for (int i = 0; i < F; ++i)
+                    fac[i] = __ldcg(a.sx + (int64_t)(list[min((32 * i + lane) % N, cnt - 1)] >> 16) * CB + cb) * sw[i];
+                if (n + kFillWarps < n_up) {
+                    cb += kFillWarps;
+                    advance();
                 }
                 if (!(ok = mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, a.status))) break;
-#pragma unroll 1
-                for (int j0 = 0; j0 < cnt; j0 += 2) {
-                    const uint4 v = v0;
-                    const int j = j0 + half;
-                    v0 = v1;
-                    v1 = load(j + 4);
-                    *reinterpret_cast<uint4*>(B + j * 128 + (((hl & 7) ^ (j & 7)) << 4)) = v;
-                }
-#pragma unroll
-                for (int i = 0; i < 2 * N / 32; ++i) f[32 * i + lane] = fac[i];
-                fence_async_shared();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(full_bar(stage));
+                store_rows(v, smem + stage * K::kStage + kABytes, cnt);
+                publish(fac);
                 next();
+            }
+        }
+        if (ok && d0 < d1) ok = wait_all(&a.head->h_done, h_bar);
+        if (ok && n < n_all) {
+            int cb = cd.a, g = cd.c, k2 = cd.d + n - n_up;
+            float sw[F];
+            auto advance = [&]() {
 #pragma unroll 1
-                for (k2 += kFillWarps; k2 >= IB2; k2 -= IB2)
+                for (; k2 >= IB2; k2 -= IB2)
                     if (++g == G) g = 0, ++cb;
+#pragma unroll
+                for (int i = 0; i < F; ++i)
+                    sw[i] = __ldg(a.sw_dn + ((int64_t)group_e(s_groups[g]) * CB + cb) * IB +
+                                  min(2 * k2 + (32 * i + lane) / N, IB - 1));
+            };
+            advance();
+#pragma unroll 1
+            while (n < n_all) {
+                const uint32_t gr = s_groups[g];
+                const int cnt = group_n(gr);
+                const uint32_t* list = s_list + group_first(gr);
+                const bool two = 2 * k2 + 1 < IB;
+                uint4 v[N / 4], w[N / 4];
+                load_rows(v, a.hq + 256 * k2, a.I, list, 0, cnt);
+                if (two) load_rows(w, a.hq + 256 * k2 + 128, a.I, list, 0, cnt);
+                float fac[F];
+#pragma unroll
+                for (int i = 0; i < F; ++i) {
+                    const int idx = 32 * i + lane, p = list[min(idx % N, cnt - 1)] & 0xFFFFu;
+                    fac[i] = __ldcg(a.sh + (int64_t)p * IB + min(2 * k2 + idx / N, IB - 1)) * sw[i] * s_w[p];
+                }
+                if (n + kFillWarps < n_all) {
+                    k2 += kFillWarps;
+                    advance();
+                }
+                if (!(ok = mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, a.status))) break;
+                uint8_t* B = smem + stage * K::kStage + kABytes;
+                store_rows(v, B, cnt);
+                if (two) store_rows(w, B + N * 128, cnt);
+                publish(fac);
+                next();
             }
         }
     } else if (warp >= 4) {
@@ -795,11 +830,8 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
                 const int cnt = group_n(gr);
                 const uint32_t* list = s_list + group_first(gr);
                 const int ub = u * CB, ue = ub + CB;
-                bool finish = true;
-                if (ub >= u0 && ue <= u1) {
-#pragma unroll
-                    for (int i = 0; i < 2 * N; ++i) my_acc[i * 128] = acc[i];
-                } else {
+                if (ub < u0) {
+                    // begun by an earlier CTA, which joins it
                     float* my = part_of(cta, up, ub) + row;
 #pragma unroll
                     for (int j = 0; j < N; ++j)
@@ -808,23 +840,19 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
                             __stcg(my + (N + j) * 128, acc[N + j]);
                         }
                     if (!(ok = meet())) break;
-                    const int c0 = up.owner(ub), c1 = up.owner(ue - 1);
-                    if (warp == 4 && lane == 0) {
-                        __threadfence();
-                        const uint32_t limit = (uint32_t)(c1 - c0);
-                        const uint32_t old = atomicInc(&a.head->up_count[c0], limit);   // back to 0 after the last
-                        if (old > limit) fg8::set_status(a.status, FG8_ERR_WORKSPACE_SHARED);
-                        s_last[joint & 1u] = old >= limit;
-                    }
-                    if (!(ok = meet())) break;
-                    finish = s_last[joint & 1u] != 0;
-                    if (finish) {
-                        __threadfence();
-#pragma unroll 2
+                    if (warp == 4 && lane == 0) st_release_gpu(&a.head->up_done[cta], *s_call);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 2 * N; ++i) my_acc[i * 128] = acc[i];
+                    if (ue > u1) {   // the later CTAs' parts
+                        const int c1 = up.owner(ue - 1);
+                        if (warp == 4) wait_calls(&a.head->up_done[cta + 1], 1, c1 - cta, *s_call, lane, abort_flag, a.status);
+                        if (!(ok = meet() && !*abort_flag)) break;
+#pragma unroll 1
                         for (int j = 0; j < cnt; ++j) {
-                            float sg = 0.f, su = 0.f;
+                            float sg = my_acc[j * 128], su = my_acc[(N + j) * 128];
 #pragma unroll 4
-                            for (int c = c0; c <= c1; ++c) {
+                            for (int c = cta + 1; c <= c1; ++c) {
                                 const float* pp = part_of(c, up, ub) + j * 128 + row;
                                 sg += __ldcg(pp);
                                 su += __ldcg(pp + N * 128);
@@ -833,12 +861,10 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
                             my_acc[(N + j) * 128] = su;
                         }
                     }
-                }
-                if (finish) {
                     // h = silu(gate) up for this row's column of every token, one
                     // 1x128 tile a token over the 128 threads
                     float* red = s_red + (joint & 1u) * 4 * N;
-#pragma unroll 2
+#pragma unroll 1
                     for (int j = 0; j < cnt; ++j) {
                         const float h = silu_mul(my_acc[j * 128], my_acc[(N + j) * 128]);
                         my_acc[j * 128] = h;
@@ -846,7 +872,7 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
                         if (lane == 0) red[quarter * N + j] = __uint_as_float(m);
                     }
                     if (!(ok = meet())) break;
-#pragma unroll 2
+#pragma unroll 1
                     for (int j = 0; j < cnt; ++j) {
                         const float m = fmaxf(fmaxf(red[j], red[N + j]), fmaxf(red[2 * N + j], red[3 * N + j]));
                         const float sc = fg8::tile_scale_fast(m);
@@ -964,14 +990,16 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 struct Layout {
-    size_t hq, sh, part, total;
+    size_t xq, sx, hq, sh, part, total;
     int64_t part_floats;
 };
-Layout layout(int64_t T, int k, int64_t I) {
+Layout layout(int64_t T, int k, int64_t C, int64_t I) {
     Layout l;
     const int64_t R = T * k;
     l.part_floats = 128 * (T > 64 ? T : 64);   // 2 N columns of a group, or T tokens
-    l.hq = kHeadBytes;
+    l.xq = kHeadBytes;
+    l.sx = l.xq + round256((size_t)(T * C));
+    l.hq = l.sx + round256((size_t)(T * (C / 128) * 4));
     l.sh = l.hq + round256((size_t)(R * I));
     l.part = l.sh + round256((size_t)(R * (I / 128) * 4));
     l.total = l.part + (size_t)(2 * kMaxCtas * l.part_floats * 4);
@@ -997,9 +1025,8 @@ fg8_status launch(const CUtensorMap& up, const CUtensorMap& dn, Args& a, cudaStr
 }  // namespace
 
 extern "C" size_t fg8_moe_decode_workspace(int64_t T, int k, int64_t C, int64_t I) {
-    (void)C;
-    if (T < 1 || T > kMaxT || k < 1 || k > fg8::kRouteMaxK || I < 128) return 0;
-    return layout(T, k, I).total;
+    if (T < 1 || T > kMaxT || k < 1 || k > fg8::kRouteMaxK || C < 128 || I < 128) return 0;
+    return layout(T, k, C, I).total;
 }
 
 extern "C" fg8_status fg8_moe_decode(const uint16_t* x, int64_t T, int C, const float* logits, const float* bias,
@@ -1024,7 +1051,7 @@ extern "C" fg8_status fg8_moe_decode(const uint16_t* x, int64_t T, int C, const 
           reinterpret_cast<uintptr_t>(topk_ids) | reinterpret_cast<uintptr_t>(affinity) |
           reinterpret_cast<uintptr_t>(sw_up) | reinterpret_cast<uintptr_t>(sw_dn)) & 3))
         return FG8_ERR_INVALID_ARG;
-    const Layout l = layout(T, k, I);
+    const Layout l = layout(T, k, C, I);
     if (ws_bytes < l.total) return FG8_ERR_INVALID_ARG;
     CUtensorMap up, dn;
     if (!fg8h::make_tensor_map_2d(&up, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, wq_up, (uint64_t)E * 2 * I, (uint64_t)C, 128,
@@ -1040,6 +1067,8 @@ extern "C" fg8_status fg8_moe_decode(const uint16_t* x, int64_t T, int C, const 
     a.k_magic = k == 1 ? 0u : (uint32_t)(((1ull << 32) + k - 1) / k);
     a.normalize = normalize; a.out_f32 = out_dtype == FG8_OUT_F32; a.out = out;
     a.head = reinterpret_cast<Head*>(ws);
+    a.xq = ws + l.xq;
+    a.sx = reinterpret_cast<float*>(ws + l.sx);
     a.hq = ws + l.hq;
     a.sh = reinterpret_cast<float*>(ws + l.sh);
     a.part = reinterpret_cast<float*>(ws + l.part);
