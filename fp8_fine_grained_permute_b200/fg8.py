@@ -149,18 +149,21 @@ def _check(status: int, what: str) -> None:
 def _ptr(t):
     if t is None:
         return None
+    try:
+        if t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError("expected a torch.Tensor or None")
     if not t.is_cuda:
         raise ValueError("libfg8 takes CUDA tensors only (no CPU fallback)")
-    if not t.is_contiguous():
-        raise ValueError("libfg8 takes contiguous tensors")
-    return t.data_ptr()
+    raise ValueError("libfg8 takes contiguous tensors")
 
 
 def _stream(stream) -> int:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:   # the current stream's handle, without building a Stream object
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -368,15 +371,21 @@ def _out(t, shape, dtype, device):
     """The caller's output tensor, checked, or a new one."""
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+    if t.shape != shape or t.dtype is not dtype:
         raise ValueError(f"output of shape {tuple(t.shape)} {t.dtype}, expected {tuple(shape)} {dtype}")
     return t
 
 
 def _want(what, t, shape, dtype):
     """Check an input tensor that a helper derives no size from."""
-    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
+    if t is not None and (t.shape != shape or t.dtype is not dtype):
         raise ValueError(f"{what} of shape {tuple(t.shape)} {t.dtype}, expected {tuple(shape)} {dtype}")
+
+
+def _want_n(what, t, n, dtype):
+    """As _want, for a tensor of n elements of any shape."""
+    if t.numel() != n or t.dtype is not dtype:
+        raise ValueError(f"{what} of {t.numel()} {t.dtype}, expected {n} {dtype}")
 
 
 def new_status(device=None) -> torch.Tensor:
@@ -603,7 +612,7 @@ def gate_weights(token_row, affinity, R, normalize=True, row_w=None, stream=None
     """token_row int32 [T*k], affinity fp32 [T, k] -> row_w fp32 [R]: the combine's
     gate weight of every routed row (0 where no slot names the row)."""
     T, k = affinity.shape
-    _want("token_row", token_row.reshape(-1), (T * k,), torch.int32)
+    _want_n("token_row", token_row, T * k, torch.int32)
     _want("affinity", affinity, (T, k), torch.float32)
     if row_w is None:
         row_w = torch.zeros(R, dtype=torch.float32, device=affinity.device)
@@ -619,8 +628,8 @@ def gate_backward(gate_dot, token_row, topk_ids, affinity, E, normalize=True, da
     nb, R = gate_dot.shape
     T, k = affinity.shape
     _want("gate_dot", gate_dot, (nb, R), torch.float32)
-    _want("token_row", token_row.reshape(-1), (T * k,), torch.int32)
-    _want("topk_ids", topk_ids.reshape(-1), (T * k,), torch.int32)
+    _want_n("token_row", token_row, T * k, torch.int32)
+    _want_n("topk_ids", topk_ids, T * k, torch.int32)
     _want("affinity", affinity, (T, k), torch.float32)
     daffinity = _out(daffinity, (T, k), torch.float32, affinity.device)
     dlogits = _out(dlogits, (T, E), torch.float32, affinity.device)
