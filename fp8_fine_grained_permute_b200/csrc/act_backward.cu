@@ -18,13 +18,16 @@
 //   * CTA = 512 threads, one persistent worker per SM; the (tile, column block)
 //     items are cut into contiguous ranges, one a CTA.  TMA brings an item's
 //     32 + 16 + 16 KB into one of two stages while the item before is worked on.
-//   * thread = 4 columns x 8 rows (a warp reads whole 128-byte code rows), dG, dU
-//     and w h of these 32 elements in 96 registers.
+//   * thread = 4 columns x 8 rows (a warp reads whole 128-byte code rows); dG and
+//     w silu(g) of these 32 elements stay in 64 registers between the pass that
+//     finds the maxima and the one that forms the codes.
 //   * a row's maximum is one warp reduction, and its codes are one 128-byte store
 //     a warp; the column maxima of the 16 warps meet in shared memory.
 //   * the column codes (8 tokens of a column a thread) are turned around through
 //     shared memory, 8-byte pieces XOR-swizzled by column, and leave as 128-byte
 //     lines of the token axis.
+#include <type_traits>
+
 #include "fg8_columns.cuh"
 #include "fg8_tma.cuh"
 
@@ -44,11 +47,11 @@ constexpr uint32_t kStage = kDhBytes + 2 * kCodeBytes;             // 64 KB
 constexpr uint32_t kOffTrans = 2 * kStage;                         // [3][128 columns][128 tokens]
 constexpr uint32_t kOffColMax = kOffTrans + 3 * kCodeBytes;        // float [16][3][128]
 constexpr uint32_t kOffColInv = kOffColMax + 4 * kWarps * 384;     // float [3][128]
-constexpr uint32_t kOffScales = kOffColInv + 4 * 384;              // float [2][3][128]
-constexpr uint32_t kOffBars = kOffScales + 2 * 4 * 384;            // 2 mbarriers, abort flag
+constexpr uint32_t kOffScales = kOffColInv + 4 * 384;              // float4 [2][128]: gate scale, up scale, weight
+constexpr uint32_t kOffBars = kOffScales + 2 * 16 * 128;            // 2 mbarriers, abort flag
 constexpr uint32_t kOffPref = kOffBars + 32;                       // int32 [kColsMaxE + 1]
 constexpr uint32_t kOffWarp = kOffPref + 4 * (fg8::kColsMaxE + 4); // int32 [36]
-constexpr uint32_t kSmemBytes = kOffWarp + 4 * 36 + 128;           // + alignment slack
+constexpr uint32_t kSmemBytes = kOffWarp + 4 * 36;
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 
 struct Args {
@@ -79,18 +82,33 @@ FG8_DEV float rcp(float x) {
     return y;
 }
 
-// code pair of (x, y) / s: with the reciprocal, or the division for a subnormal scale
-FG8_DEV uint32_t code2(float x, float y, float inv) {
-    return fg8::cvt_e4m3x2(fg8::mul_f32x2(fg8::pack_f32x2(x, y), fg8::pack_f32x2(inv, inv)));
+// max(|a|, |b|, |c|), one instruction on sm_100
+FG8_DEV float max3_abs(float a, float b, float c) {
+    float d;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
-FG8_DEV uint32_t code1_exact(float x, float s) { return fg8::cvt_e4m3x2(__fdiv_rn(x, s), 0.f) & 0xFFu; }
+
+// codes of v times r (or, exactly, v over the scale r: for subnormal scales),
+// the first in bits 7..0
+template <bool kExact>
+FG8_DEV uint32_t code2(float2 v, float2 r) {
+    const float2 z = kExact ? make_float2(__fdiv_rn(v.x, r.x), __fdiv_rn(v.y, r.y)) : __fmul2_rn(v, r);
+    return fg8::cvt_e4m3x2(z.x, z.y);
+}
+// the same for two tokens of a column; `inv` is the reciprocal, or a subnormal
+// scale negated
+template <bool kExact>
+FG8_DEV uint32_t code_pair(float x, float y, float inv) {
+    if (kExact && inv < 0.f) return fg8::cvt_e4m3x2(__fdiv_rn(x, -inv), __fdiv_rn(y, -inv));
+    return fg8::cvt_e4m3x2(x * inv, y * inv);
+}
+FG8_DEV float2 splat(float x) { return make_float2(x, x); }
 
 __global__ void __launch_bounds__(kThreads, 1)
 act_backward(const __grid_constant__ CUtensorMap tm_dh, const __grid_constant__ CUtensorMap tm_gu,
              const Args a) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
+    extern __shared__ __align__(128) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
     float* s_colmax = reinterpret_cast<float*>(smem + kOffColMax);
     float* s_colinv = reinterpret_cast<float*>(smem + kOffColInv);
@@ -111,155 +129,144 @@ act_backward(const __grid_constant__ CUtensorMap tm_dh, const __grid_constant__ 
     if (blockIdx.x == 0)
         for (int e = tid; e <= a.E; e += kThreads) a.offsets_out[e] = 128 * s_pref[e];
 
-    const int64_t tiles = min((int64_t)s_pref[a.E], a.P / 128);
-    const int64_t items = tiles * ncb;
-    const int64_t i0 = items * blockIdx.x / gridDim.x, i1 = items * (blockIdx.x + 1) / gridDim.x;
+    const int tiles = (int)min((int64_t)s_pref[a.E], a.P / 128);
+    const int64_t items = (int64_t)tiles * ncb;
+    const int owned = min(a.offsets[a.E], (int)a.R);   // rows from here on belong to no expert
+    const int i0 = (int)(items * blockIdx.x / gridDim.x), i1 = (int)(items * (blockIdx.x + 1) / gridDim.x);
     if (i0 >= i1) return;
 
-    auto tile_of = [&](int64_t it) {
-        return fg8::find_tile((int)(it / ncb), s_pref, a.offsets, a.E, a.R);
-    };
-    auto issue = [&](int64_t it, const fg8::RowTile& t, int st) {   // one thread
-        const int cb = (int)(it % ncb), y = (int)max((int64_t)0, min(t.row0, a.R - 1));
+    auto tile_of = [&](int tile) { return fg8::find_tile(tile, s_pref, a.offsets, a.E, (int)a.R); };
+    auto issue = [&](int cb, int row0, int st) {   // one thread
         const uint32_t dst = sbase + st * kStage;
         mbar_arrive_expect_tx(full_bar(st), kStage);
-        tma_load_2d(&tm_dh, dst, full_bar(st), 128 * cb, y);
-        tma_load_2d(&tm_gu, dst + kDhBytes, full_bar(st), 128 * cb, y);
-        tma_load_2d(&tm_gu, dst + kDhBytes + kCodeBytes, full_bar(st), a.I + 128 * cb, y);
+        tma_load_2d(&tm_dh, dst, full_bar(st), 128 * cb, row0);
+        tma_load_2d(&tm_gu, dst + kDhBytes, full_bar(st), 128 * cb, row0);
+        tma_load_2d(&tm_gu, dst + kDhBytes + kCodeBytes, full_bar(st), a.I + 128 * cb, row0);
     };
-    // this thread's one of an item's 3 x 128 row factors: gate scale, up scale, weight
-    auto load_factor = [&](int64_t it, const fg8::RowTile& t) {
+    // one of an item's 3 x 128 row factors a thread, 0 for the rows of others;
+    // asynchronous, so that nothing waits for it in the pass it is issued in
+    auto load_factor = [&](int cb, const fg8::RowTile& t, int st) {
         const int which = tid >> 7, r = tid & 127;
-        if (which > 2 || r >= t.n_in) return 0.f;
-        const int64_t row = t.row0 + r;
-        if (which == 2) return a.row_w ? __ldg(a.row_w + row) : 1.0f;
-        return __ldg(a.sgu + (int64_t)((which ? ncb : 0) + (int)(it % ncb)) * a.R + row);
+        if (which > 2) return;
+        float* dst = s_scales + 512 * st + 4 * r + which;
+        if (which == 2 && a.row_w == nullptr) {
+            *dst = r < t.n_in ? 1.0f : 0.f;
+            return;
+        }
+        const float* src = which == 2 ? a.row_w : a.sgu + (int64_t)((which ? ncb : 0) + cb) * a.R;
+        const uint32_t bytes = r < t.n_in ? 4u : 0u;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)),
+                     "l"(src + (bytes ? t.row0 + r : 0)), "r"(bytes)
+                     : "memory");
     };
+    auto factors_landed = [] { asm volatile("cp.async.wait_all;" ::: "memory"); };
 
-    fg8::RowTile cur = tile_of(i0);
+    fg8::RowTile cur = tile_of(i0 / ncb);
+    int cb = i0 % ncb;
     if (tid == 0) {
-        issue(i0, cur, 0);
-        if (i0 + 1 < i1) issue(i0 + 1, tile_of(i0 + 1), 1);
+        issue(cb, cur.row0, 0);
+        if (i0 + 1 < i1) {
+            if (cb + 1 < ncb) issue(cb + 1, cur.row0, 1);
+            else issue(0, tile_of(cur.tile + 1).row0, 1);
+        }
     }
-    if (tid < 384) s_scales[tid] = load_factor(i0, cur);
+    load_factor(cb, cur, 0);
+    factors_landed();
     __syncthreads();
 
     bool ok = true;
-    for (int64_t it = i0; it < i1; ++it) {
-        const int n = (int)(it - i0), st = n & 1;
-        const int cb = (int)(it % ncb);
-        fg8::RowTile nxt = cur;
-        float next_factor = 0.f;
+    for (int it = i0; it < i1; ++it) {
+        const int n = it - i0, st = n & 1;
         if (it + 1 < i1) {
-            if ((it + 1) % ncb == 0) nxt = tile_of(it + 1);
-            next_factor = load_factor(it + 1, nxt);
+            if (cb + 1 < ncb) load_factor(cb + 1, cur, st ^ 1);
+            else load_factor(0, tile_of(cur.tile + 1), st ^ 1);
         }
-        const float* fac = s_scales + 384 * st;
+        const float4* fac = reinterpret_cast<const float4*>(s_scales + 512 * st);
         const uint8_t* sdh = smem + st * kStage + 8 * lane;
         const uint8_t* sg = smem + st * kStage + kDhBytes + 4 * lane;
         const int r0 = kRows * warp;
         ok = mbar_wait(full_bar(st), (n >> 1) & 1, abort_flag, a.status);
 
-        // ---- values of 8 rows x 4 columns
-        float dG[kRows][4], dU[kRows][4], H[kRows][4];
-        float dot[kRows];
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const int r = r0 + i;
-            dot[i] = 0.f;
-            if (r < cur.n_in) {   // warp-uniform; padding rows take no part
-                const uint32_t gw = *reinterpret_cast<const uint32_t*>(sg + r * 128);
-                const uint32_t uw = *reinterpret_cast<const uint32_t*>(sg + kCodeBytes + r * 128);
-                const uint2 dw = *reinterpret_cast<const uint2*>(sdh + r * 256);
-                const float fg = fac[r], fu = fac[128 + r], w = fac[256 + r];
-                const float2 g2[2] = {fg8::e4m3x2_f32(gw & 0xFFFFu), fg8::e4m3x2_f32(gw >> 16)};
-                const float2 u2[2] = {fg8::e4m3x2_f32(uw & 0xFFFFu), fg8::e4m3x2_f32(uw >> 16)};
-                const float gc[4] = {g2[0].x, g2[0].y, g2[1].x, g2[1].y};
-                const float uc[4] = {u2[0].x, u2[0].y, u2[1].x, u2[1].y};
-                const float dc[4] = {fg8::bf16_lo(dw.x), fg8::bf16_hi(dw.x), fg8::bf16_lo(dw.y),
-                                     fg8::bf16_hi(dw.y)};
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const float g = gc[c] * fg, u = uc[c] * fu;
-                    // exp2's argument is clamped so that 1 + e stays finite (and
-                    // its reciprocal above the flushed range): sig >= 2^-125
-                    const float sig = rcp(1.0f + ex2(fminf(g * -1.4426950408889634f, 125.0f)));
-                    const float silu = g * sig, h = silu * u;
-                    dot[i] = fmaf(dc[c], h, dot[i]);
-                    const float d = dc[c] * w;
-                    dU[i][c] = d * silu;
-                    dG[i][c] = d * u * sig * (1.0f + fmaf(-g, sig, g));
-                    H[i][c] = h * w;
-                }
-            } else {
-#pragma unroll
-                for (int c = 0; c < 4; ++c) dG[i][c] = dU[i][c] = H[i][c] = 0.f;
+        // rows that no expert owns may hold anything: zeros in their place (the rows
+        // of a tile that belong to the next expert are finite; their factors are 0)
+        if (cur.n_in < 128 && cur.row0 + 128 > owned) {
+            const int first = max(cur.n_in, owned - cur.row0);
+            uint8_t* stage = smem + st * kStage;
+            for (int i = tid; i < (128 - first) * 32; i += kThreads) {
+                const int r = first + (i >> 5), l = i & 31;
+                *reinterpret_cast<uint2*>(stage + r * 256 + 8 * l) = make_uint2(0u, 0u);
+                *reinterpret_cast<uint32_t*>(stage + kDhBytes + r * 128 + 4 * l) = 0u;
+                *reinterpret_cast<uint32_t*>(stage + kDhBytes + kCodeBytes + r * 128 + 4 * l) = 0u;
             }
+            fence_async_shared();   // before the stage's next TMA load
+            __syncthreads();
         }
-        // ---- column maxima of this warp's rows
-        {
-            float m[3][4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                m[0][c] = m[1][c] = m[2][c] = 0.f;
-#pragma unroll
-                for (int i = 0; i < kRows; ++i) {
-                    m[0][c] = fmaxf(m[0][c], fabsf(dG[i][c]));
-                    m[1][c] = fmaxf(m[1][c], fabsf(dU[i][c]));
-                    m[2][c] = fmaxf(m[2][c], fabsf(H[i][c]));
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < 3; ++k)
-                *reinterpret_cast<float4*>(s_colmax + warp * 384 + k * 128 + 4 * lane) =
-                    make_float4(m[k][0], m[k][1], m[k][2], m[k][3]);
-        }
-        // all warps' maxima are there, and the stage has been read
-        if (!__syncthreads_and(ok)) {
-            ok = false;
-            break;
-        }
-        if (tid == 0 && it + 2 < i1) issue(it + 2, (it + 2) / ncb == it / ncb ? cur : tile_of(it + 2), st);
 
-        // ---- by rows: lane i < 16 owns the scale of row i & 7 of dG (i < 8) or dU
+        // ---- first pass over 8 rows x 4 columns, column pairs in packed
+        // arithmetic.  dG and S = w silu(g) stay in registers; dU = dh S and
+        // w h = u S are formed again in the second pass from the staged inputs
+        // (all three would not leave the compiler the registers it needs).
+        float2 dG[kRows][2], S[kRows][2];
+        float row_max = 0.f;   // lane i < 16: of row i & 7 of dG (i < 8) or dU
         {
-            float mine = 0.f;
+            float dot[kRows];
+            float4 mG = make_float4(0.f, 0.f, 0.f, 0.f), mU = mG, mH = mG;
+            auto fold = [](float4& m, const float2 (&a)[2], const float2 (&b)[2]) {
+                m.x = max3_abs(m.x, a[0].x, b[0].x);
+                m.y = max3_abs(m.y, a[0].y, b[0].y);
+                m.z = max3_abs(m.z, a[1].x, b[1].x);
+                m.w = max3_abs(m.w, a[1].y, b[1].y);
+            };
 #pragma unroll
-            for (int i = 0; i < kRows; ++i) {
-                const float mg = fmaxf(fmaxf(fabsf(dG[i][0]), fabsf(dG[i][1])), fmaxf(fabsf(dG[i][2]), fabsf(dG[i][3])));
-                const float mu = fmaxf(fmaxf(fabsf(dU[i][0]), fabsf(dU[i][1])), fmaxf(fabsf(dU[i][2]), fabsf(dU[i][3])));
-                const uint32_t xg = __reduce_max_sync(kFull, __float_as_uint(mg));
-                const uint32_t xu = __reduce_max_sync(kFull, __float_as_uint(mu));
-                if (lane == i) mine = __uint_as_float(xg);
-                if (lane == kRows + i) mine = __uint_as_float(xu);
-            }
-            const float s = fg8::tile_scale_fast(mine);
-            const float inv = fg8::inv_scale(s);
-            const int my_row = r0 + (lane & 7);
-            if (lane < 16 && my_row < cur.n_in)
-                a.sd[(int64_t)((lane >> 3) * ncb + cb) * a.R + cur.row0 + my_row] = s;
-            const bool sub = __any_sync(kFull, lane < 16 && fg8::scale_subnormal(s));
-            uint8_t* out = a.dq + (cur.row0 + r0) * (2 * (int64_t)a.I) + 128 * cb + 4 * lane;
+            for (int i = 0; i < kRows; i += 2) {
+                float2 dU[2][2], H[2][2];
 #pragma unroll
-            for (int i = 0; i < kRows; ++i) {
-                const float ig = __shfl_sync(kFull, inv, i), iu = __shfl_sync(kFull, inv, kRows + i);
-                uint32_t cg = code2(dG[i][0], dG[i][1], ig) | (code2(dG[i][2], dG[i][3], ig) << 16);
-                uint32_t cu = code2(dU[i][0], dU[i][1], iu) | (code2(dU[i][2], dU[i][3], iu) << 16);
-                if (sub) {
-                    const float sg_ = __shfl_sync(kFull, s, i), su_ = __shfl_sync(kFull, s, kRows + i);
-                    cg = cu = 0u;
+                for (int h = 0; h < 2; ++h) {
+                    const int r = r0 + i + h;
+                    const uint32_t gw = *reinterpret_cast<const uint32_t*>(sg + r * 128);
+                    const uint32_t uw = *reinterpret_cast<const uint32_t*>(sg + kCodeBytes + r * 128);
+                    const uint2 dw = *reinterpret_cast<const uint2*>(sdh + r * 256);
+                    const float4 f4 = fac[r];
+                    const float2 fg = splat(f4.x), fu = splat(f4.y), w = splat(f4.z);
+                    float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        cg |= code1_exact(dG[i][c], sg_) << (8 * c);
-                        cu |= code1_exact(dU[i][c], su_) << (8 * c);
+                    for (int p = 0; p < 2; ++p) {
+                        const float2 g = __fmul2_rn(fg8::e4m3x2_f32(p ? gw >> 16 : gw & 0xFFFFu), fg);
+                        const float2 u = __fmul2_rn(fg8::e4m3x2_f32(p ? uw >> 16 : uw & 0xFFFFu), fu);
+                        const uint32_t db = p ? dw.y : dw.x;
+                        const float2 dh = make_float2(fg8::bf16_lo(db), fg8::bf16_hi(db));
+                        // exp overflows to infinity for very negative gates: sig is 0 then
+                        const float2 t = __fmul2_rn(g, splat(-1.4426950408889634f));
+                        const float2 q = __fadd2_rn(make_float2(ex2(t.x), ex2(t.y)), splat(1.0f));
+                        const float2 sig = make_float2(rcp(q.x), rcp(q.y));
+                        const float2 silu = __fmul2_rn(g, sig);
+                        sum = __ffma2_rn(dh, __fmul2_rn(silu, u), sum);
+                        const float2 sw = __fmul2_rn(silu, w);
+                        dU[h][p] = __fmul2_rn(dh, sw);
+                        H[h][p] = __fmul2_rn(u, sw);
+                        // 1 + g (1 - sig)
+                        const float2 f = __ffma2_rn(silu, splat(-1.0f), __fadd2_rn(g, splat(1.0f)));
+                        dG[i + h][p] = __fmul2_rn(__fmul2_rn(__fmul2_rn(dh, w), __fmul2_rn(u, sig)), f);
+                        S[i + h][p] = sw;
                     }
+                    dot[i + h] = sum.x + sum.y;
+                    const float2 (&vG)[2] = dG[i + h];
+                    const float2 (&vU)[2] = dU[h];
+                    const uint32_t xg = __reduce_max_sync(
+                        kFull, __float_as_uint(max3_abs(max3_abs(vG[0].x, vG[0].y, vG[1].x), vG[1].y, 0.f)));
+                    const uint32_t xu = __reduce_max_sync(
+                        kFull, __float_as_uint(max3_abs(max3_abs(vU[0].x, vU[0].y, vU[1].x), vU[1].y, 0.f)));
+                    if (lane == i + h) row_max = __uint_as_float(xg);
+                    if (lane == kRows + i + h) row_max = __uint_as_float(xu);
                 }
-                if (r0 + i < cur.n_in) {
-                    uint8_t* o = out + (int64_t)i * (2 * (int64_t)a.I);
-                    *reinterpret_cast<uint32_t*>(o) = cg;
-                    *reinterpret_cast<uint32_t*>(o + a.I) = cu;
-                }
+                fold(mG, dG[i], dG[i + 1]);
+                fold(mU, dU[0], dU[1]);
+                fold(mH, H[0], H[1]);
             }
+            float4* cm = reinterpret_cast<float4*>(s_colmax + warp * 384) + lane;
+            cm[0] = mG;
+            cm[32] = mU;
+            cm[64] = mH;
             // the rows' dots: 8 values over 32 lanes, halved at each exchange
             if (a.gate_dot) {
                 float v4[4], v2[2], v1;
@@ -283,61 +290,143 @@ act_backward(const __grid_constant__ CUtensorMap tm_dh, const __grid_constant__ 
                 if ((lane & 3) == 0 && r < cur.n_in) a.gate_dot[(int64_t)cb * a.R + cur.row0 + r] = v1;
             }
         }
+        // row scales, a lane each
+        const float row_s = fg8::tile_scale_fast(row_max), row_inv = fg8::inv_scale(row_s);
+        {
+            const int my_row = r0 + (lane & 7);
+            if (lane < 16 && my_row < cur.n_in)
+                a.sd[(int64_t)((lane >> 3) * ncb + cb) * a.R + cur.row0 + my_row] = row_s;
+        }
+        // all warps' maxima are there
+        if (!__syncthreads_and(ok)) {
+            ok = false;
+            break;
+        }
         // ---- column scales
         if (tid < 384) {
             float m = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_colmax[w * 384 + tid]);
+            for (int w = 0; w < kWarps; w += 2)
+                m = max3_abs(m, s_colmax[w * 384 + tid], s_colmax[(w + 1) * 384 + tid]);
             const float s = fg8::tile_scale_fast(m);
             // a subnormal scale is handed on negated: its codes take the division
             s_colinv[tid] = fg8::scale_subnormal(s) ? -s : fg8::inv_scale(s);
             const int which = tid >> 7, c = 128 * cb + (tid & 127);
-            const int64_t pt = cur.pcol / 128;
+            const int64_t pt = cur.tile;
             if (which < 2) a.sdT[pt * (2 * (int64_t)a.I) + which * (int64_t)a.I + c] = s;
             else a.shT[pt * (int64_t)a.I + c] = s;
         }
         __syncthreads();
 
-        // ---- by columns: 8 tokens of 4 columns of the three matrices
+        // ---- second pass: codes by rows (a 128-byte line a warp and row) and by
+        // columns (8 tokens of a column a thread, in pairs of tokens)
+        {
+            const float4* ci = reinterpret_cast<const float4*>(s_colinv) + lane;
+            bool divide = fg8::scale_subnormal(row_s);
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
-            const float4 i4 = *reinterpret_cast<const float4*>(s_colinv + 128 * k + 4 * lane);
-            const float inv[4] = {i4.x, i4.y, i4.z, i4.w};
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                float v[kRows];
-#pragma unroll
-                for (int i = 0; i < kRows; ++i) v[i] = k == 0 ? dG[i][c] : k == 1 ? dU[i][c] : H[i][c];
-                uint2 q;
-                if (inv[c] < 0.f) {
-                    q = make_uint2(0u, 0u);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        q.x |= code1_exact(v[i], -inv[c]) << (8 * i);
-                        q.y |= code1_exact(v[4 + i], -inv[c]) << (8 * i);
-                    }
-                } else {
-                    q.x = code2(v[0], v[1], inv[c]) | (code2(v[2], v[3], inv[c]) << 16);
-                    q.y = code2(v[4], v[5], inv[c]) | (code2(v[6], v[7], inv[c]) << 16);
-                }
-                *reinterpret_cast<uint2*>(smem + kOffTrans + k * kCodeBytes + (4 * lane + c) * 128 +
-                                          8 * (warp ^ (lane & 15))) = q;
+            for (int k = 0; k < 3; ++k) {
+                const float4 v = ci[32 * k];
+                divide |= fminf(fminf(v.x, v.y), fminf(v.z, v.w)) < 0.f;
             }
-        }
-        if (tid < 384 && it + 1 < i1) s_scales[384 * (st ^ 1) + tid] = next_factor;
-        __syncthreads();
+            divide = __any_sync(kFull, divide);
+            const int rows = cur.n_in - r0;
+            uint8_t* out = a.dq + (int64_t)(cur.row0 + r0) * (2 * a.I) + 128 * cb + 4 * lane;
+            uint2 code[3][4];   // [dG, dU, w h][column]: 8 tokens
+            auto four = [&](int i, auto exact) {   // rows i .. i + 3, one matrix after the other (registers)
+                constexpr bool kExact = decltype(exact)::value;
+                auto by_rows = [&](const float2 (&v)[4][2], int src, int at) {
 #pragma unroll
-        for (int j = 0; j < 3 * 128 * 8 / kThreads; ++j) {
-            const int u = tid + kThreads * j, k = u >> 10, col = (u >> 3) & 127, p = u & 7;
-            const int f = (col >> 2) & 15;
-            uint4 v = *reinterpret_cast<const uint4*>(smem + kOffTrans + k * kCodeBytes + col * 128 +
-                                                      16 * (p ^ (f >> 1)));
-            if (f & 1) v = make_uint4(v.z, v.w, v.x, v.y);
-            const int64_t c = 128 * cb + col;
-            uint8_t* o = k < 2 ? a.dqT + (k * (int64_t)a.I + c) * a.P : a.hqT + c * a.P;
-            *reinterpret_cast<uint4*>(o + cur.pcol + 16 * p) = v;
+                    for (int h = 0; h < 4; ++h) {
+                        const float2 r = splat(__shfl_sync(kFull, kExact ? row_s : row_inv, src + i + h));
+                        const uint32_t w = __byte_perm(code2<kExact>(v[h][0], r), code2<kExact>(v[h][1], r), 0x5410);
+                        if (i + h < rows) *reinterpret_cast<uint32_t*>(out + (i + h) * (2 * a.I) + at) = w;
+                    }
+                };
+                auto by_columns = [&](const float2 (&v)[4][2], int k) {
+                    const float4 inv = ci[32 * k];
+                    const uint32_t q[4] = {
+                        __byte_perm(code_pair<kExact>(v[0][0].x, v[1][0].x, inv.x), code_pair<kExact>(v[2][0].x, v[3][0].x, inv.x), 0x5410),
+                        __byte_perm(code_pair<kExact>(v[0][0].y, v[1][0].y, inv.y), code_pair<kExact>(v[2][0].y, v[3][0].y, inv.y), 0x5410),
+                        __byte_perm(code_pair<kExact>(v[0][1].x, v[1][1].x, inv.z), code_pair<kExact>(v[2][1].x, v[3][1].x, inv.z), 0x5410),
+                        __byte_perm(code_pair<kExact>(v[0][1].y, v[1][1].y, inv.w), code_pair<kExact>(v[2][1].y, v[3][1].y, inv.w), 0x5410)};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) (i ? code[k][c].y : code[k][c].x) = q[c];
+                };
+                float2 v[4][2];
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    v[h][0] = dG[i + h][0];
+                    v[h][1] = dG[i + h][1];
+                }
+                by_rows(v, 0, 0);
+                by_columns(v, 0);
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    const uint2 dw = *reinterpret_cast<const uint2*>(sdh + (r0 + i + h) * 256);
+                    v[h][0] = __fmul2_rn(make_float2(fg8::bf16_lo(dw.x), fg8::bf16_hi(dw.x)), S[i + h][0]);
+                    v[h][1] = __fmul2_rn(make_float2(fg8::bf16_lo(dw.y), fg8::bf16_hi(dw.y)), S[i + h][1]);
+                }
+                by_rows(v, kRows, a.I);
+                by_columns(v, 1);
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    const uint32_t uw = *reinterpret_cast<const uint32_t*>(sg + kCodeBytes + (r0 + i + h) * 128);
+                    const float2 fu = splat(fac[r0 + i + h].y);
+                    v[h][0] = __fmul2_rn(__fmul2_rn(fg8::e4m3x2_f32(uw & 0xFFFFu), fu), S[i + h][0]);
+                    v[h][1] = __fmul2_rn(__fmul2_rn(fg8::e4m3x2_f32(uw >> 16), fu), S[i + h][1]);
+                }
+                by_columns(v, 2);
+            };
+            if (!divide) {
+                four(0, std::false_type());
+                four(4, std::false_type());
+            } else {
+                four(0, std::true_type());
+                four(4, std::true_type());
+            }
+            if (rows < kRows) {   // padding tokens: code 0 (not the code of -0)
+                const int k0 = max(0, min(4, rows)), k1 = max(0, min(4, rows - 4));
+                const uint32_t m0 = k0 == 4 ? 0xFFFFFFFFu : (1u << (8 * k0)) - 1u;
+                const uint32_t m1 = k1 == 4 ? 0xFFFFFFFFu : (1u << (8 * k1)) - 1u;
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) code[k][c] = make_uint2(code[k][c].x & m0, code[k][c].y & m1);
+            }
+            uint8_t* base = smem + kOffTrans + 4 * lane * 128 + 8 * (warp ^ (lane & 15));
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) *reinterpret_cast<uint2*>(base + k * kCodeBytes + c * 128) = code[k][c];
         }
-        cur = nxt;
+        factors_landed();
+        __syncthreads();   // the turned codes are there, and the stage has been read
+        if (tid == 0 && it + 2 < i1) {
+            const int up = (cb + 2) / ncb;   // tiles further on
+            issue(cb + 2 - up * ncb, up ? tile_of(cur.tile + up).row0 : cur.row0, st);
+        }
+        {
+            // 16 bytes of a column a thread: columns tid / 8 and 64 further on
+            const int c0 = tid >> 3, p = tid & 7, f = (c0 >> 2) & 15;   // (col >> 2) & 15 is the same for both
+            const uint8_t* src = smem + kOffTrans + c0 * 128 + 16 * (p ^ (f >> 1));
+            uint8_t* dst[3];
+            dst[0] = a.dqT + (int64_t)(128 * cb + c0) * a.P + 128 * (int64_t)cur.tile + 16 * p;
+            dst[1] = dst[0] + (int64_t)a.I * a.P;
+            dst[2] = a.hqT + (dst[0] - a.dqT);
+            const int64_t half = 64 * a.P;
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint4 v = *reinterpret_cast<const uint4*>(src + k * kCodeBytes + h * 64 * 128);
+                    if (f & 1) v = make_uint4(v.z, v.w, v.x, v.y);
+                    *reinterpret_cast<uint4*>(dst[k] + h * half) = v;
+                }
+        }
+        if (++cb == ncb) {
+            cb = 0;
+            if (it + 1 < i1) cur = tile_of(cur.tile + 1);
+        }
     }
     if (!ok && tid == 0) {   // let copies already issued land before the CTA winds down
         const uint64_t t0 = fg8::globaltimer_ns();
@@ -357,7 +446,7 @@ extern "C" fg8_status fg8_swiglu_backward_quant(const uint16_t* dh, const uint8_
                                                 fg8_stream_t stream) {
     if (R < 0 || I < 128 || I % 128 || E < 1) return FG8_ERR_INVALID_ARG;
     if (!offsets || !offsets_out) return FG8_ERR_INVALID_ARG;
-    if (E > fg8::kColsMaxE || R > INT32_MAX || I > INT32_MAX / 2) return FG8_ERR_UNSUPPORTED;
+    if (E > fg8::kColsMaxE || R > INT32_MAX || I > INT32_MAX / 32) return FG8_ERR_UNSUPPORTED;
     if (R == 0)
         return cudaMemsetAsync(offsets_out, 0, sizeof(int32_t) * ((size_t)E + 1), (cudaStream_t)stream) ==
                        cudaSuccess ? FG8_OK : FG8_ERR_CUDA;
@@ -386,6 +475,7 @@ extern "C" fg8_status fg8_swiglu_backward_quant(const uint16_t* dh, const uint8_
     a.dq = dq; a.sd = sd; a.dqT = dqT; a.sdT = sdT; a.hqT = hqT; a.shT = shT;
     a.gate_dot = gate_dot; a.offsets_out = offsets_out; a.status = dev_status;
     const int64_t most = (R / 128 + E) * (int64_t)(I / 128);
+    if (most > INT32_MAX) return FG8_ERR_UNSUPPORTED;
     int64_t grid = fg8h::num_sms();
     if (grid > most) grid = most;
     act_backward<<<(unsigned)grid, kThreads, kSmemBytes, (cudaStream_t)stream>>>(m_dh, m_gu, a);

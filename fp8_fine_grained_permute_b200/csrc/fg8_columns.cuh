@@ -37,29 +37,28 @@ FG8_DEV float inv_scale(float s) {
 }
 FG8_DEV bool scale_subnormal(float s) { return !(s >= 1.17549435e-38f); }
 
-// One 128-row tile of an expert in the padded token axis.
+// One 128-row tile of an expert in the padded token axis (tile number `tile`:
+// padded columns from 128 * tile).
 struct RowTile {
-    int64_t row0;   // first logical row
-    int n_in;       // rows of the expert in it (>= 1, <= 128)
-    int64_t pcol;   // first padded column
+    int row0;   // first logical row
+    int n_in;   // rows of the expert in it (<= 128; 0 if the offsets are not of this buffer)
+    int tile;
 };
 
 // s_pref: exclusive prefix of tiles per expert (s_pref[E] = all tiles);
 // offsets as the caller gave them; R rows exist.
-FG8_DEV RowTile find_tile(int tile, const int32_t* s_pref, const int32_t* offsets, int E, int64_t R) {
+FG8_DEV RowTile find_tile(int tile, const int32_t* s_pref, const int32_t* offsets, int E, int R) {
     int lo = 0, hi = E;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (s_pref[mid] <= tile) lo = mid; else hi = mid;
     }
-    const int tb = tile - s_pref[lo];
-    const int32_t o0 = offsets[lo], o1 = offsets[lo + 1];
+    const int64_t r0 = (int64_t)offsets[lo] + 128 * (int64_t)(tile - s_pref[lo]);
     RowTile t;
-    t.row0 = (int64_t)o0 + 128 * (int64_t)tb;
+    t.tile = tile;
+    t.row0 = r0 < 0 || r0 >= R ? 0 : (int)r0;
     // rows that the buffers do not hold (offsets inconsistent with R) are not touched
-    t.n_in = (int)max((int64_t)0, min((int64_t)min(128, o1 - o0 - 128 * tb), R - t.row0));
-    if (t.row0 < 0) t.n_in = 0;
-    t.pcol = (int64_t)128 * tile;
+    t.n_in = r0 < 0 || r0 >= R ? 0 : (int)min((int64_t)min(128, R - t.row0), offsets[lo + 1] - r0);
     return t;
 }
 

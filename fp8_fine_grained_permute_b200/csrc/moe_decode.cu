@@ -328,8 +328,8 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
     using K = Cfg<N>;
     constexpr int S = K::kStages;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    // (an offset keeps the pointer a shared-memory one for the compiler)
+    uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
     const uint32_t sbase = smem_u32(smem);
     const uint32_t bar0 = sbase + K::kOffBars;
     auto full_bar = [&](int s) { return bar0 + 8u * s; };

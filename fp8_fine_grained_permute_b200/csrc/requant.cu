@@ -76,11 +76,11 @@ __global__ void __launch_bounds__(kThreads, 2) requant_columns(const Args a) {
         for (int e = tid; e <= a.E; e += kThreads) a.offsets_out[e] = 128 * s_pref[e];
     const int tile = blockIdx.x;
     if (tile >= s_pref[a.E] || 128 * (int64_t)tile + 128 > a.P) return;
-    const fg8::RowTile t = fg8::find_tile(tile, s_pref, a.offsets, a.E, a.R);
+    const fg8::RowTile t = fg8::find_tile(tile, s_pref, a.offsets, a.E, (int)a.R);
     if (tid < 128) {
         int32_t src = -1;
         if (tid < t.n_in) {
-            const int64_t v = a.row_token ? (int64_t)a.row_token[t.row0 + tid] : t.row0 + tid;
+            const int64_t v = a.row_token ? (int64_t)a.row_token[t.row0 + tid] : (int64_t)t.row0 + tid;
             if (v >= 0 && v < a.T) src = (int32_t)v;
             else fg8::set_status(a.status, FG8_ERR_INVALID_ARG);
         }
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 2) requant_columns(const Args a) {
             const int u = tid + kThreads * j, col = u >> 3, p = u & 7;
             const uint4 v = *reinterpret_cast<const uint4*>(smem + kOffTrans + col * 128 +
                                                             16 * (p ^ ((col >> 2) & 7)));
-            *reinterpret_cast<uint4*>(a.xqT + (int64_t)(128 * cb + col) * a.P + t.pcol + 16 * p) = v;
+            *reinterpret_cast<uint4*>(a.xqT + (int64_t)(128 * cb + col) * a.P + 128 * (int64_t)tile + 16 * p) = v;
         }
     }
 }
