@@ -17,6 +17,21 @@ FG8_DEV float2 e4m3x2_f32(uint32_t codes) {
     return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// Four E4M3 codes -> two pairs of fp32 values, without taking the word apart.
+FG8_DEV void e4m3x4_f32(uint32_t codes, float2& lo, float2& hi) {
+    uint32_t a, b;
+    asm("{\n"
+        ".reg .b16 l, h;\n"
+        "mov.b32 {l, h}, %2;\n"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n"
+        "cvt.rn.f16x2.e4m3x2 %1, h;\n"
+        "}\n"
+        : "=r"(a), "=r"(b)
+        : "r"(codes));
+    lo = __half22float2(*reinterpret_cast<const __half2*>(&a));
+    hi = __half22float2(*reinterpret_cast<const __half2*>(&b));
+}
+
 // The scale of a tile of fp32 values without the division routine: q = amax /
 // 448 from the rounded reciprocal and one residual correction, the IEEE quotient
 // for every amax >= 2^-110 (checked over all of them); below that the division.

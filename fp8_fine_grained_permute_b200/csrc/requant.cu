@@ -18,30 +18,27 @@
 // to 2^-45 before its own rounding to fp32.  (In that order, on -x and -r, the
 // sign of a zero survives: z0 + (x - z0 sT) r turns -0 into +0.)
 //
-// CTA = 256 threads on one 128-token tile of an expert and a group of its
-// 128-column blocks; cp.async gathers the next block's 16 KB while this one is
-// converted.  Thread = 4 columns x 16 tokens: a warp reads whole 128-byte rows,
-// the 8 warps' column maxima meet in shared memory, and the codes are turned
-// around there too (16-byte pieces, XOR-swizzled by column) to leave as
-// 128-byte lines.
+// CTA = 256 threads, two a SM, with a contiguous range of (128-token tile, 128
+// columns) items each; cp.async gathers two items ahead.  A warp owns 16 columns
+// of all 128 tokens, a thread 4 columns x 16 tokens: the column maxima are 16
+// values in a thread and three shuffles, a thread's codes of a column are 16
+// consecutive bytes, and the 8 lanes of a column write its whole 128-byte line --
+// no exchange through shared memory and one barrier an item.
 #include "fg8_columns.cuh"
 #include "fg8_tma.cuh"
 
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kRows = 128 / kWarps;                  // tokens of a thread: 16
-constexpr uint32_t kTile = 128 * 128;                // one block's codes
-constexpr uint32_t kOffTrans = 2 * kTile;            // [128 columns][128 tokens]
-constexpr uint32_t kOffMax = kOffTrans + kTile;      // float [8][128]
-constexpr uint32_t kOffCol = kOffMax + 4 * kWarps * 128;   // float2 [128]: scale, reciprocal
-constexpr uint32_t kOffScale = kOffCol + 8 * 128;    // float [2][128]: row scales
-constexpr uint32_t kOffPref = kOffScale + 2 * 4 * 128;
+constexpr int kRows = 16;                            // tokens of a thread
+constexpr int kCtasPerSm = 2;
+constexpr int kStages = 3;
+constexpr uint32_t kTile = 128 * 128;                // an item's codes
+constexpr uint32_t kScalePitch = 20;                 // floats from 16 rows' scales to the next 16: conflict-free 16-byte reads
+constexpr uint32_t kOffScale = kStages * kTile;      // float [stages][8][20]
+constexpr uint32_t kOffPref = kOffScale + kStages * 4 * 8 * kScalePitch;
 constexpr uint32_t kOffWarp = kOffPref + 4 * (fg8::kColsMaxE + 4);
-constexpr uint32_t kOffRows = kOffWarp + 4 * 36;     // int32 [128]
-constexpr uint32_t kSmemBytes = kOffRows + 4 * 128;
-constexpr int kColGroups = 4;                        // column groups per tile (grid.y)
+constexpr uint32_t kSmemBytes = kOffWarp + 4 * 36;
 
 struct Args {
     const uint8_t* xq;        // [T][K]
@@ -56,164 +53,181 @@ struct Args {
     int32_t* status;
 };
 
-FG8_DEV uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-
-__global__ void __launch_bounds__(kThreads, 2) requant_columns(const Args a) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) requant_columns(const Args a) {
     extern __shared__ __align__(128) uint8_t smem[];
-    float* s_max = reinterpret_cast<float*>(smem + kOffMax);
-    float2* s_col = reinterpret_cast<float2*>(smem + kOffCol);
     float* s_scale = reinterpret_cast<float*>(smem + kOffScale);
     int32_t* s_pref = reinterpret_cast<int32_t*>(smem + kOffPref);
-    int32_t* s_rows = reinterpret_cast<int32_t*>(smem + kOffRows);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int word = lane & 3, group = lane >> 2;   // columns 16 warp + 4 word .., tokens 16 group ..
 
     fg8::tile_prefix(a.offsets, a.E, s_pref, reinterpret_cast<int32_t*>(smem + kOffWarp));
-    if (blockIdx.x == 0 && blockIdx.y == 0)
+    if (blockIdx.x == 0)
         for (int e = tid; e <= a.E; e += kThreads) a.offsets_out[e] = 128 * s_pref[e];
-    const int tile = blockIdx.x;
-    if (tile >= s_pref[a.E] || 128 * (int64_t)tile + 128 > a.P) return;
-    const fg8::RowTile t = fg8::find_tile(tile, s_pref, a.offsets, a.E, (int)a.R);
-    if (tid < 128) {
-        int32_t src = -1;
-        if (tid < t.n_in) {
-            const int64_t v = a.row_token ? (int64_t)a.row_token[t.row0 + tid] : (int64_t)t.row0 + tid;
-            if (v >= 0 && v < a.T) src = (int32_t)v;
-            else fg8::set_status(a.status, FG8_ERR_INVALID_ARG);
-        }
-        s_rows[tid] = src;
-    }
-    __syncthreads();
     const int ncb = (int)(a.K / 128);
-    const int cb0 = (int)((int64_t)ncb * blockIdx.y / gridDim.y), cb1 = (int)((int64_t)ncb * (blockIdx.y + 1) / gridDim.y);
-    if (cb0 >= cb1) return;
+    const int tiles = (int)min((int64_t)s_pref[a.E], a.P / 128);
+    const int64_t items = (int64_t)tiles * ncb;
+    const int64_t i0 = items * blockIdx.x / gridDim.x;
+    int left = (int)(items * (blockIdx.x + 1) / gridDim.x - i0);   // items to go
+    if (left == 0) return;
+    int tile = (int)(i0 / ncb), cb = (int)(i0 % ncb);
 
-    const int32_t my_src = s_rows[tid & 127];
-    auto issue = [&](int cb, int st) {
+    // What a thread gathers: 16 bytes of rows tid / 8, 32, 64 and 96 further on, and
+    // (the first 128) a row's scale.  Chunk c of row r stands at c ^ (r / 16 mod 8):
+    // the 8 token groups that a warp reads together are on different banks.
+    const uint8_t* src[4];
+    const float* src_scale = nullptr;
+    uint32_t src_ok = 0;   // bits 0..3: the rows exist (padding: zeros); bit 4: the scale's
+    int ahead_tile = tile, ahead_cb = cb, ahead = left, ahead_stage = 0;
+    auto find_sources = [&](int t, int c) {   // for item (t, c) and the ones after it in the tile
+        const fg8::RowTile rt = fg8::find_tile(t, s_pref, a.offsets, a.E, (int)a.R);
+        auto source = [&](int r) {
+            if (r >= rt.n_in) return (int64_t)-1;
+            const int64_t v = a.row_token ? (int64_t)a.row_token[rt.row0 + r] : (int64_t)rt.row0 + r;
+            if (v >= 0 && v < a.T) return v;
+            fg8::set_status(a.status, FG8_ERR_INVALID_ARG);
+            return (int64_t)-1;
+        };
+        src_ok = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int u = tid + kThreads * j, r = u >> 3, ch = u & 7;
-            const int32_t src = s_rows[r];
-            const uint8_t* p = a.xq + (src >= 0 ? (int64_t)src * a.K + 128 * cb + 16 * ch : 0);
-            const uint32_t n = src >= 0 ? 16u : 0u;   // rows of padding: zeros
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                             fg8::tma::smem_u32(smem + st * kTile + 16 * u)),
-                         "l"(p), "r"(n)
-                         : "memory");
+            const int64_t v = source((tid >> 3) + 32 * j);
+            src_ok |= (uint32_t)(v >= 0) << j;
+            src[j] = a.xq + max(v, (int64_t)0) * a.K + 128 * (int64_t)c + 16 * (tid & 7);
         }
         if (tid < 128) {
-            const uint32_t n = my_src >= 0 ? 4u : 0u;
-            const float* p = a.sx + (my_src >= 0 ? (int64_t)cb * a.T + my_src : 0);
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
-                             fg8::tma::smem_u32(s_scale + 128 * st + tid)),
-                         "l"(p), "r"(n)
-                         : "memory");
+            const int64_t v = source(tid);
+            src_ok |= (uint32_t)(v >= 0) << 4;
+            src_scale = a.sx + (int64_t)c * a.T + max(v, (int64_t)0);
+        }
+    };
+    const uint32_t sbase = fg8::tma::smem_u32(smem);
+    auto issue = [&]() {   // the next item of the CTA's range, if there is one
+        if (ahead > 0) {
+            --ahead;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int r = (tid >> 3) + 32 * j;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                 sbase + ahead_stage * kTile + 128 * r + 16 * ((tid & 7) ^ (r >> 4))),
+                             "l"(src[j]), "r"(src_ok >> j & 1u ? 16u : 0u)
+                             : "memory");
+                src[j] += 128;
+            }
+            if (tid < 128) {
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
+                                 sbase + kOffScale + 4 * (ahead_stage * 8 * kScalePitch + (tid >> 4) * kScalePitch + (tid & 15))),
+                             "l"(src_scale), "r"(src_ok & 16u ? 4u : 0u)
+                             : "memory");
+                src_scale += a.T;
+            }
+            if (++ahead_stage == kStages) ahead_stage = 0;
+            if (++ahead_cb == ncb) {
+                ahead_cb = 0;
+                ++ahead_tile;
+                if (ahead > 0) find_sources(ahead_tile, 0);
+            }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    issue(cb0, 0);
-    for (int cb = cb0; cb < cb1; ++cb) {
-        const int st = (cb - cb0) & 1;
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        __syncthreads();   // this block is there; the other stage and the transposed codes have been read
-        if (cb + 1 < cb1) issue(cb + 1, st ^ 1);
+    find_sources(tile, cb);
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue();
 
-        // 16 tokens x 4 columns, negated
-        uint64_t x[kRows][2];
-        float m[4] = {0.f, 0.f, 0.f, 0.f};
-        const uint8_t* src = smem + st * kTile + (kRows * warp) * 128 + 4 * lane;
-        const float* sc = s_scale + 128 * st + kRows * warp;
+    const int col0 = 16 * warp + 4 * word;
+    uint8_t* out = a.xqT + ((int64_t)128 * cb + col0) * a.P + 128 * (int64_t)tile + 16 * group;
+    for (int st = 0; left > 0; --left) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+        __syncthreads();   // this item is there, and the stage of the item before has been read
+        issue();
+        float4 sc[kRows / 4];
+#pragma unroll
+        for (int i = 0; i < kRows / 4; ++i)
+            sc[i] = reinterpret_cast<const float4*>(s_scale + (st * 8 + group) * kScalePitch)[i];
+        const uint8_t* in = smem + st * kTile + kRows * group * 128 + 16 * (warp ^ group) + 4 * word;
+        // 16 tokens x 4 columns, negated; largest and smallest of each column (a
+        // three-input maximum takes no absolute values)
+        float2 x[kRows][2];
+        float hi[4] = {0.f, 0.f, 0.f, 0.f}, lo[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(src + 128 * i);
-            const float s = -sc[i];
-            const float2 v0 = fg8::e4m3x2_f32(w & 0xFFFFu), v1 = fg8::e4m3x2_f32(w >> 16);
-            const float2 p0 = __fmul2_rn(v0, make_float2(s, s)), p1 = __fmul2_rn(v1, make_float2(s, s));
-            x[i][0] = fg8::pack_f32x2(p0.x, p0.y);
-            x[i][1] = fg8::pack_f32x2(p1.x, p1.y);
-            m[0] = fmaxf(m[0], fabsf(p0.x));
-            m[1] = fmaxf(m[1], fabsf(p0.y));
-            m[2] = fmaxf(m[2], fabsf(p1.x));
-            m[3] = fmaxf(m[3], fabsf(p1.y));
+            float2 v0, v1;
+            fg8::e4m3x4_f32(*reinterpret_cast<const uint32_t*>(in + 128 * i), v0, v1);
+            const float s = i % 4 == 0 ? sc[i / 4].x : i % 4 == 1 ? sc[i / 4].y : i % 4 == 2 ? sc[i / 4].z : sc[i / 4].w;
+            x[i][0] = __fmul2_rn(v0, make_float2(-s, -s));
+            x[i][1] = __fmul2_rn(v1, make_float2(-s, -s));
         }
-        *reinterpret_cast<float4*>(s_max + 128 * warp + 4 * lane) = make_float4(m[0], m[1], m[2], m[3]);
-        __syncthreads();
-        if (tid < 128) {
-            float mm = s_max[tid];
 #pragma unroll
-            for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, s_max[128 * w + tid]);
-            const float s = fg8::tile_scale_fast(mm);
-            // reciprocal 0: the quotient's residual would leave the normal range
-            // (scales below 2^-100), these codes take the division
-            s_col[tid] = make_float2(s, s >= 0x1p-100f ? __frcp_rn(s) : 0.f);
-            a.saT[(int64_t)tile * a.K + 128 * cb + tid] = s;
+        for (int i = 0; i < kRows; ++i) {
+            hi[0] = fmaxf(hi[0], x[i][0].x), lo[0] = fminf(lo[0], x[i][0].x);
+            hi[1] = fmaxf(hi[1], x[i][0].y), lo[1] = fminf(lo[1], x[i][0].y);
+            hi[2] = fmaxf(hi[2], x[i][1].x), lo[2] = fminf(lo[2], x[i][1].x);
+            hi[3] = fmaxf(hi[3], x[i][1].y), lo[3] = fminf(lo[3], x[i][1].y);
         }
-        __syncthreads();
-        float sT[4], r[4];
+        float m[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) m[c] = fmaxf(hi[c], -lo[c]);
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) m[c] = fmaxf(m[c], __shfl_xor_sync(0xffffffffu, m[c], o));
+        // scale and reciprocal: lane group g works out column g mod 4 and hands it round
+        const float mine = group & 2 ? (group & 1 ? m[3] : m[2]) : (group & 1 ? m[1] : m[0]);
+        const float s_mine = fg8::tile_scale_fast(mine);
+        // reciprocal 0: the quotient's residual would leave the normal range (scales
+        // below 2^-100), these codes take the division
+        const float r_mine = s_mine >= 0x1p-100f ? -__frcp_rn(s_mine) : 0.f;
+        if (group < 4) a.saT[(int64_t)tile * a.K + 128 * cb + col0 + group] = s_mine;
+        float s[4], r[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            const float2 v = s_col[4 * lane + c];
-            sT[c] = v.x;
-            r[c] = v.y;
+            s[c] = __shfl_sync(0xffffffffu, s_mine, 4 * c + word);
+            r[c] = __shfl_sync(0xffffffffu, r_mine, 4 * c + word);
         }
-        uint32_t code[kRows / 4][4];   // [token group][column]: 4 tokens a word
-        const bool tiny = r[0] == 0.f || r[1] == 0.f || r[2] == 0.f || r[3] == 0.f;
-        if (!tiny) {
-            const uint64_t rr[2] = {fg8::pack_f32x2(-r[0], -r[1]), fg8::pack_f32x2(-r[2], -r[3])};
-            const uint64_t ss[2] = {fg8::pack_f32x2(sT[0], sT[1]), fg8::pack_f32x2(sT[2], sT[3])};
+        if (!__any_sync(0xffffffffu, r_mine == 0.f)) {
 #pragma unroll
-            for (int g = 0; g < kRows / 4; ++g) {
-                uint32_t w[4];   // token i's four codes, columns in bytes
+            for (int p = 0; p < 2; ++p) {
+                const float2 s2 = make_float2(s[2 * p], s[2 * p + 1]), nr = make_float2(r[2 * p], r[2 * p + 1]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t h[2];
-#pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        const uint64_t xv = x[4 * g + i][p];
-                        const uint64_t z0 = fg8::mul_f32x2(xv, rr[p]);
-                        h[p] = fg8::cvt_e4m3x2(fma_f32x2(fma_f32x2(z0, ss[p], xv), rr[p], z0));
-                    }
-                    w[i] = h[0] | (h[1] << 16);
+                for (int i = 0; i < kRows; ++i) {
+                    const float2 z0 = __fmul2_rn(x[i][p], nr);
+                    x[i][p] = __ffma2_rn(__ffma2_rn(z0, s2, x[i][p]), nr, z0);
                 }
-                // 4 x 4 bytes turned: column words of 4 tokens
-                const uint32_t a0 = __byte_perm(w[0], w[1], 0x5140), a1 = __byte_perm(w[2], w[3], 0x5140);
-                const uint32_t b0 = __byte_perm(w[0], w[1], 0x7362), b1 = __byte_perm(w[2], w[3], 0x7362);
-                code[g][0] = __byte_perm(a0, a1, 0x5410);
-                code[g][1] = __byte_perm(a0, a1, 0x7632);
-                code[g][2] = __byte_perm(b0, b1, 0x5410);
-                code[g][3] = __byte_perm(b0, b1, 0x7632);
             }
         } else {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                const float sc_ = c == 0 ? s[0] : c == 1 ? s[1] : c == 2 ? s[2] : s[3];
 #pragma unroll
-            for (int g = 0; g < kRows / 4; ++g) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c) code[g][c] = 0u;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float v[4];
-                    asm("mov.b64 {%0, %1}, %2;" : "=f"(v[0]), "=f"(v[1]) : "l"(x[4 * g + i][0]));
-                    asm("mov.b64 {%0, %1}, %2;" : "=f"(v[2]), "=f"(v[3]) : "l"(x[4 * g + i][1]));
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        code[g][c] |= (fg8::cvt_e4m3x2(__fdiv_rn(-v[c], sT[c]), 0.f) & 0xFFu) << (8 * i);
+                for (int i = 0; i < kRows; ++i) {
+                    const float v = c & 1 ? (c & 2 ? x[i][1].y : x[i][0].y) : (c & 2 ? x[i][1].x : x[i][0].x);
+                    const float z = __fdiv_rn(-v, sc_);
+                    if (c == 0) x[i][0].x = z;
+                    if (c == 1) x[i][0].y = z;
+                    if (c == 2) x[i][1].x = z;
+                    if (c == 3) x[i][1].y = z;
                 }
             }
         }
-        // 16 tokens of a column: piece `warp` of its 128 bytes, at warp ^ (lane & 7)
+        // 16 tokens of a column are 16 bytes
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-            *reinterpret_cast<uint4*>(smem + kOffTrans + (4 * lane + c) * 128 + 16 * (warp ^ (lane & 7))) =
-                make_uint4(code[0][c], code[1][c], code[2][c], code[3][c]);
-        __syncthreads();
+        for (int c = 0; c < 4; ++c) {
+            uint32_t q[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int u = tid + kThreads * j, col = u >> 3, p = u & 7;
-            const uint4 v = *reinterpret_cast<const uint4*>(smem + kOffTrans + col * 128 +
-                                                            16 * (p ^ ((col >> 2) & 7)));
-            *reinterpret_cast<uint4*>(a.xqT + (int64_t)(128 * cb + col) * a.P + 128 * (int64_t)tile + 16 * p) = v;
+            for (int h = 0; h < 4; ++h) {
+                float z[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) z[i] = c & 1 ? x[4 * h + i][c >> 1].y : x[4 * h + i][c >> 1].x;
+                q[h] = __byte_perm(fg8::cvt_e4m3x2(z[0], z[1]), fg8::cvt_e4m3x2(z[2], z[3]), 0x5410);
+            }
+            *reinterpret_cast<uint4*>(out + c * a.P) = make_uint4(q[0], q[1], q[2], q[3]);
+        }
+        if (++st == kStages) st = 0;
+        if (++cb == ncb) {
+            cb = 0;
+            ++tile;
+            out = a.xqT + (int64_t)col0 * a.P + 128 * (int64_t)tile + 16 * group;
+        } else {
+            out += 128 * a.P;
         }
     }
 }
@@ -245,7 +259,11 @@ extern "C" fg8_status fg8_requantize_colwise(const uint8_t* xq, const float* sx,
     if (cudaFuncSetAttribute(requant_columns, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) !=
         cudaSuccess)
         return FG8_ERR_CUDA;
-    const dim3 grid((unsigned)(R / 128 + E), (unsigned)kColGroups);
-    requant_columns<<<grid, kThreads, kSmemBytes, (cudaStream_t)stream>>>(a);
+    const int64_t most = (R / 128 + E) * (K / 128);
+    if (R / 128 + E > INT32_MAX) return FG8_ERR_UNSUPPORTED;
+    int64_t grid = (int64_t)kCtasPerSm * fg8h::num_sms();
+    if (grid > most) grid = most;
+    if (most / grid > INT32_MAX) return FG8_ERR_UNSUPPORTED;
+    requant_columns<<<(unsigned)grid, kThreads, kSmemBytes, (cudaStream_t)stream>>>(a);
     return fg8h::launch_status();
 }
