@@ -636,10 +636,10 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
             }
             if ((slot += kFillWarps) >= K::kSlots) slot -= K::kSlots;
         };
-        // all CTAs have written what this one reads next: fill warp 0 watches, the
-        // others wait for it here
-        auto wait_all = [&](const uint32_t* arrivals, uint32_t bar) {
-            if (fw == 0 && lane == 0) {
+        // all CTAs have written what this one reads next: the fill warp that comes
+        // first watches, the others wait for it here
+        auto wait_all = [&](const uint32_t* arrivals, uint32_t bar, int watch) {
+            if (fw == watch && lane == 0) {
                 const uint32_t all = *s_call * (uint32_t)ctas;
                 const uint64_t t0 = fg8::globaltimer_ns();
                 while ((int32_t)(fg8::ld_acquire_gpu(arrivals) - all) < 0 && !*abort_flag) {
@@ -682,8 +682,7 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
             __syncwarp();
             if (lane == 0) mbar_arrive(full_bar(stage));
         };
-        ok = n_all == 0 || wait_all(&a.head->x_done, x_bar);
-        if (ok && n < n_up) {
+        if (n < n_up) {
             int cb = cu.b + n, g = cu.c, ib = cu.d;
             // block scales of a step, loaded a step ahead (they come from HBM)
             float sw[F];
@@ -696,8 +695,9 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
                     sw[i] = __ldg(a.sw_up + ((int64_t)group_e(s_groups[g]) * 2 * IB + ib + (32 * i + lane) / N * IB) * CB + cb);
             };
             advance();
+            ok = wait_all(&a.head->x_done, x_bar, 0);
 #pragma unroll 1
-            while (n < n_up) {
+            while (ok && n < n_up) {
                 const uint32_t gr = s_groups[g];
                 const int cnt = group_n(gr);
                 const uint32_t* list = s_list + group_first(gr);
@@ -717,7 +717,6 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
                 next();
             }
         }
-        if (ok && d0 < d1) ok = wait_all(&a.head->h_done, h_bar);
         if (ok && n < n_all) {
             int cb = cd.a, g = cd.c, k2 = cd.d + n - n_up;
             float sw[F];
@@ -731,8 +730,9 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
                                   min(2 * k2 + (32 * i + lane) / N, IB - 1));
             };
             advance();
+            ok = wait_all(&a.head->h_done, h_bar, n_up % kFillWarps);
 #pragma unroll 1
-            while (n < n_all) {
+            while (ok && n < n_all) {
                 const uint32_t gr = s_groups[g];
                 const int cnt = group_n(gr);
                 const uint32_t* list = s_list + group_first(gr);
@@ -849,22 +849,19 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
                         if (warp == 4) wait_calls(&a.head->up_done[cta + 1], 1, c1 - cta, *s_call, lane, abort_flag, a.status);
                         if (!(ok = meet() && !*abort_flag)) break;
 #pragma unroll 1
-                        for (int j = 0; j < cnt; ++j) {
-                            float sg = my_acc[j * 128], su = my_acc[(N + j) * 128];
+                        for (int c = cta + 1; c <= c1; ++c) {
+                            const float* pp = part_of(c, up, ub) + row;
 #pragma unroll 4
-                            for (int c = cta + 1; c <= c1; ++c) {
-                                const float* pp = part_of(c, up, ub) + j * 128 + row;
-                                sg += __ldcg(pp);
-                                su += __ldcg(pp + N * 128);
+                            for (int j = 0; j < cnt; ++j) {
+                                my_acc[j * 128] += __ldcg(pp + j * 128);
+                                my_acc[(N + j) * 128] += __ldcg(pp + (N + j) * 128);
                             }
-                            my_acc[j * 128] = sg;
-                            my_acc[(N + j) * 128] = su;
                         }
                     }
                     // h = silu(gate) up for this row's column of every token, one
                     // 1x128 tile a token over the 128 threads
                     float* red = s_red + (joint & 1u) * 4 * N;
-#pragma unroll 1
+#pragma unroll 2
                     for (int j = 0; j < cnt; ++j) {
                         const float h = silu_mul(my_acc[j * 128], my_acc[(N + j) * 128]);
                         my_acc[j * 128] = h;
@@ -872,7 +869,7 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
                         if (lane == 0) red[quarter * N + j] = __uint_as_float(m);
                     }
                     if (!(ok = meet())) break;
-#pragma unroll 1
+#pragma unroll 2
                     for (int j = 0; j < cnt; ++j) {
                         const float m = fmaxf(fmaxf(red[j], red[N + j]), fmaxf(red[2 * N + j], red[3 * N + j]));
                         const float sc = fg8::tile_scale_fast(m);
