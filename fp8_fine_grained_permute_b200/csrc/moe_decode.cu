@@ -132,19 +132,18 @@ struct Cfg {
     static_assert(sizeof(Plan) <= 128, "plan");
 };
 
-// workspace: a fixed head of counters (zero between calls), then the codes
-// and scales of x and h and the partials of cut units
-constexpr size_t kHeadBytes = FG8_MOE_DECODE_HEAD;
+// workspace: a head of counters and the partials of cut units, both at fixed places
+// and never used for anything else, then the codes and scales of x and h.  A word
+// of a partial is {call tag, fp32 value} in 64 bits, so that a reader sees from the
+// word itself that it is this call's: no flag, no fence and no second trip.
+constexpr size_t kHeadBytes = 4096;
 struct Head {
-    // call numbers order the arrivals, so nothing is cleared between calls;
-    // part_done: its part of the output block that it shares with earlier [0] or
-    // later [1] CTAs is written
-    uint32_t x_done, h_done;         // all CTAs' arrivals of all calls: codes of x, h are written
+    // arrivals are counted over all calls, so nothing is cleared between them
+    uint32_t x_done, h_done;         // CTAs that have written their codes of x, of h
     uint32_t calls[kMaxCtas];        // calls that the CTA has finished
-    uint32_t part_done[kMaxCtas][2];
-    uint32_t up_done[kMaxCtas];      // its part of a unit of h that began before its share
 };
 static_assert(sizeof(Head) <= kHeadBytes, "counter head");
+constexpr int kPartWords = 128 * 64;   // a group's gate and up (2 x 32 x 128), or 64 tokens x 128 columns
 
 struct Args {
     const uint16_t* x;
@@ -163,8 +162,7 @@ struct Args {
     float* sx;               // [T][C / 128]
     uint8_t* hq;             // [T k][I]
     float* sh;               // [T k][I / 128]
-    float* part;             // [2 CTAs][part_floats]
-    int64_t part_floats;
+    uint64_t* part;          // [2 CTAs][kPartWords]
     int32_t* status;
 };
 
@@ -186,30 +184,34 @@ FG8_DEV void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) {
         : "memory");
 }
 
-FG8_DEV void st_release_gpu(uint32_t* p, uint32_t v) {
-    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
-}
-
 FG8_DEV void red_release_gpu(uint32_t* p, uint32_t v) {
     asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
-// A warp waits until flags[0], flags[stride], .. (n of them) hold `call` (bounded:
+// partial words
+FG8_DEV void put_word(uint64_t* p, uint32_t tag, float v) {
+    asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p), "l"((uint64_t)tag << 32 | __float_as_uint(v)) : "memory");
+}
+FG8_DEV uint64_t get_word(const uint64_t* p) {
+    uint64_t v;
+    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+    return v;
+}
+FG8_DEV void get_words2(const uint64_t* p, uint64_t& a, uint64_t& b) {   // each of the two as a whole
+    asm volatile("ld.relaxed.gpu.global.v2.u64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "l"(p) : "memory");
+}
+FG8_DEV bool tagged(uint64_t w, uint32_t tag) { return (uint32_t)(w >> 32) == tag; }
+FG8_DEV float value_of(uint64_t w) { return __uint_as_float((uint32_t)w); }
+// Between two tries at words that are not all there: false to give up (bounded:
 // raises the abort flag and reports FG8_ERR_TIMEOUT).
-FG8_DEV void wait_calls(const uint32_t* flags, int stride, int n, uint32_t call, int lane, volatile int* abort_flag,
-                        int32_t* status) {
-    const uint64_t t0 = fg8::globaltimer_ns();
-    for (int i = lane; i < n; i += 32) {
-        while (fg8::ld_acquire_gpu(flags + i * stride) != call) {
-            if (*abort_flag) break;
-            if (fg8::globaltimer_ns() - t0 > fg8::kWaitLimitNs) {
-                fg8::set_status(status, FG8_ERR_TIMEOUT);
-                *abort_flag = 1;
-                break;
-            }
-        }
+__device__ __noinline__ bool try_again(uint64_t& t0, volatile int* abort_flag, int32_t* status) {
+    const uint64_t now = fg8::globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > fg8::kWaitLimitNs) {
+        fg8::set_status(status, FG8_ERR_TIMEOUT);
+        *abort_flag = 1;
     }
-    __syncwarp();
+    return !*abort_flag;
 }
 
 // E4M3 codes of 8 bf16 values over their tile's scale: the quotient as product,
@@ -642,12 +644,14 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
             if (fw == watch && lane == 0) {
                 const uint32_t all = *s_call * (uint32_t)ctas;
                 const uint64_t t0 = fg8::globaltimer_ns();
-                while ((int32_t)(fg8::ld_acquire_gpu(arrivals) - all) < 0 && !*abort_flag) {
+                int32_t over;
+                while ((over = (int32_t)(fg8::ld_acquire_gpu(arrivals) - all)) < 0 && !*abort_flag) {
                     if (fg8::globaltimer_ns() - t0 > fg8::kWaitLimitNs) {
                         fg8::set_status(a.status, FG8_ERR_TIMEOUT);
                         *abort_flag = 1;
                     }
                 }
+                if (over > 0) fg8::set_status(a.status, FG8_ERR_WORKSPACE_SHARED);   // another call arrives here too
                 mbar_arrive(bar);
             }
             __syncwarp();
@@ -807,9 +811,10 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
         };
         // where CTA c keeps its partial of a unit that begins at step `begin`
         auto part_of = [&](int c, const Share& sh, int begin) {
-            return a.part + (int64_t)(2 * c + (begin > sh.begin(c) ? 1 : 0)) * a.part_floats;
+            return a.part + (int64_t)(2 * c + (begin > sh.begin(c) ? 1 : 0)) * kPartWords;
         };
 
+        const uint32_t tag_up = 2u * *s_call, tag_dn = tag_up + 1u;   // never 0
         float* my_acc = s_acc + row;   // this thread's column, its alone
         auto clear = [&]() {
 #pragma unroll
@@ -832,29 +837,36 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
                 const int ub = u * CB, ue = ub + CB;
                 if (ub < u0) {
                     // begun by an earlier CTA, which joins it
-                    float* my = part_of(cta, up, ub) + row;
+                    uint64_t* my = part_of(cta, up, ub) + row;
 #pragma unroll
                     for (int j = 0; j < N; ++j)
                         if (j < cnt) {
-                            __stcg(my + j * 128, acc[j]);
-                            __stcg(my + (N + j) * 128, acc[N + j]);
+                            put_word(my + j * 128, tag_up, acc[j]);
+                            put_word(my + (N + j) * 128, tag_up, acc[N + j]);
                         }
-                    if (!(ok = meet())) break;
-                    if (warp == 4 && lane == 0) st_release_gpu(&a.head->up_done[cta], *s_call);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 2 * N; ++i) my_acc[i * 128] = acc[i];
                     if (ue > u1) {   // the later CTAs' parts
                         const int c1 = up.owner(ue - 1);
-                        if (warp == 4) wait_calls(&a.head->up_done[cta + 1], 1, c1 - cta, *s_call, lane, abort_flag, a.status);
-                        if (!(ok = meet() && !*abort_flag)) break;
 #pragma unroll 1
                         for (int c = cta + 1; c <= c1; ++c) {
-                            const float* pp = part_of(c, up, ub) + row;
-#pragma unroll 4
-                            for (int j = 0; j < cnt; ++j) {
-                                my_acc[j * 128] += __ldcg(pp + j * 128);
-                                my_acc[(N + j) * 128] += __ldcg(pp + (N + j) * 128);
+                            const uint64_t* pp = part_of(c, up, ub) + row;
+#pragma unroll 1
+                            for (int j0 = 0; j0 < cnt; j0 += 4) {
+                                uint64_t w[8], t0 = 0;
+                                bool all;
+                                do {
+                                    all = true;
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) {   // a token past the last: the last again
+                                        w[i] = get_word(pp + ((i & 1) * N + min(j0 + i / 2, cnt - 1)) * 128);
+                                        all &= tagged(w[i], tag_up);
+                                    }
+                                } while (!all && try_again(t0, abort_flag, a.status));
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    if (j0 + i / 2 < cnt) my_acc[((i & 1) * N + j0 + i / 2) * 128] += value_of(w[i]);
                             }
                         }
                     }
@@ -922,50 +934,53 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
 #pragma unroll 1
                     for (int t = 0; t < a.T; ++t) store_out(t, 128 * cb + row, my_acc[t * 128]);
                 } else {
-                    float* my = part_of(cta, dn, ub) + row;
+                    uint64_t* my = part_of(cta, dn, ub) + row;
 #pragma unroll 4
-                    for (int t = 0; t < a.T; ++t) __stcg(my + t * 128, my_acc[t * 128]);
-                    if (!(ok = meet())) break;
-                    if (warp == 4 && lane == 0) st_release_gpu(&a.head->part_done[cta][ub > d0], *s_call);
+                    for (int t = 0; t < a.T; ++t) put_word(my + t * 128, tag_dn, my_acc[t * 128]);
                 }
 #pragma unroll 1
                 for (int t = 0; t < a.T; ++t) my_acc[t * 128] = 0.f;
                 ++cb;
             }
-            // cut blocks (at most the first and the last of this CTA's): once all
-            // their parts are there, each of their CTAs joins its share of the
-            // T x 128 sums, four columns a thread
+            // cut blocks (at most the first and the last of this CTA's): each of their
+            // CTAs joins its share of the T x 128 sums, four columns a thread
             const int cb0 = cd.a, cb1 = plan.cur[3].b ? plan.cur[3].a : plan.cur[3].a - 1;
 #pragma unroll 1
             for (int c = cb0; ok && c <= cb1; c += max(1, cb1 - cb0)) {
                 const int ub = c * unit_dn, ue = ub + unit_dn;
                 if (ub >= d0 && ue <= d1) continue;
                 const int c0 = dn.owner(ub), c1 = dn.owner(ue - 1), n = c1 - c0 + 1;
-                // the block begins inside the first CTA's share (its later part) or
-                // with it; for all others it is their first
-                if (warp == 4) {
-                    const uint32_t* first = &a.head->part_done[c0][ub > dn.begin(c0)];
-                    wait_calls(first, 2, 1, *s_call, lane, abort_flag, a.status);
-                    wait_calls(&a.head->part_done[c0 + 1][0], 2, n - 1, *s_call, lane, abort_flag, a.status);
-                }
-                if (!(ok = meet()) || *abort_flag) break;
                 const int quads = 32 * a.T, q1 = quads * (cta - c0 + 1) / n;
 #pragma unroll 1
                 for (int q = quads * (cta - c0) / n + row; q < q1; q += 128) {
-                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-                    for (int w = c0; w <= c1; ++w) {
-                        const float4 pv = __ldcg(reinterpret_cast<const float4*>(part_of(w, dn, ub)) + q);
-                        v.x += pv.x;
-                        v.y += pv.y;
-                        v.z += pv.z;
-                        v.w += pv.w;
+                    float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+                    for (int w0 = c0; w0 <= c1; w0 += 6) {
+                        uint64_t w[6][4], t0 = 0;
+                        bool all;
+                        do {
+                            all = true;
+#pragma unroll
+                            for (int k = 0; k < 6; ++k) {   // a CTA past the last: the last again
+                                const uint64_t* pp = part_of(min(w0 + k, c1), dn, ub) + 4 * q;
+                                get_words2(pp, w[k][0], w[k][1]);
+                                get_words2(pp + 2, w[k][2], w[k][3]);
+                            }
+#pragma unroll
+                            for (int k = 0; k < 24; ++k) all &= tagged(w[k / 4][k & 3], tag_dn);
+                        } while (!all && try_again(t0, abort_flag, a.status));
+#pragma unroll
+                        for (int k = 0; k < 6; ++k) {
+                            if (w0 + k > c1) break;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) v[i] += value_of(w[k][i]);
+                        }
                     }
                     const int t = q >> 5, col = 128 * c + 4 * (q & 31);
-                    store_out(t, col, v.x);
-                    store_out(t, col + 1, v.y);
-                    store_out(t, col + 2, v.z);
-                    store_out(t, col + 3, v.w);
+                    store_out(t, col, v[0]);
+                    store_out(t, col + 1, v[1]);
+                    store_out(t, col + 2, v[2]);
+                    store_out(t, col + 3, v[3]);
                 }
             }
         }
@@ -987,21 +1002,21 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 struct Layout {
-    size_t xq, sx, hq, sh, part, total;
-    int64_t part_floats;
+    size_t part, xq, sx, hq, sh, total;
 };
 Layout layout(int64_t T, int k, int64_t C, int64_t I) {
     Layout l;
     const int64_t R = T * k;
-    l.part_floats = 128 * (T > 64 ? T : 64);   // 2 N columns of a group, or T tokens
-    l.xq = kHeadBytes;
+    l.part = kHeadBytes;
+    l.xq = l.part + sizeof(uint64_t) * 2 * kMaxCtas * kPartWords;
     l.sx = l.xq + round256((size_t)(T * C));
     l.hq = l.sx + round256((size_t)(T * (C / 128) * 4));
     l.sh = l.hq + round256((size_t)(R * I));
-    l.part = l.sh + round256((size_t)(R * (I / 128) * 4));
-    l.total = l.part + (size_t)(2 * kMaxCtas * l.part_floats * 4);
+    l.total = l.sh + round256((size_t)(R * (I / 128) * 4));
     return l;
 }
+static_assert(kPartWords >= 2 * 32 * 128 && kPartWords >= kMaxT * 128, "a part fits its slot");
+static_assert(FG8_MOE_DECODE_HEAD == kHeadBytes + sizeof(uint64_t) * 2 * kMaxCtas * kPartWords, "what the caller zeroes");
 
 template <int N>
 fg8_status launch(const CUtensorMap& up, const CUtensorMap& dn, Args& a, cudaStream_t st) {
@@ -1068,8 +1083,7 @@ extern "C" fg8_status fg8_moe_decode(const uint16_t* x, int64_t T, int C, const 
     a.sx = reinterpret_cast<float*>(ws + l.sx);
     a.hq = ws + l.hq;
     a.sh = reinterpret_cast<float*>(ws + l.sh);
-    a.part = reinterpret_cast<float*>(ws + l.part);
-    a.part_floats = l.part_floats;
+    a.part = reinterpret_cast<uint64_t*>(ws + l.part);
     a.status = dev_status;
     return T <= 16 ? launch<16>(up, dn, a, (cudaStream_t)stream) : launch<32>(up, dn, a, (cudaStream_t)stream);
 }

@@ -39,7 +39,7 @@ FG8_GROUP_M = 0
 FG8_GROUP_K = 1
 FG8_BSCALE_BLOCK128 = 0
 FG8_BSCALE_ROW128 = 1
-FG8_MOE_DECODE_HEAD = 4096
+FG8_MOE_DECODE_HEAD = 4096 + 2 * 160 * 64 * 128 * 8
 
 
 class FG8Error(RuntimeError):

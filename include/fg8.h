@@ -514,9 +514,10 @@ fg8_status fg8_grouped_gemm_combine(const uint8_t* a, const float* sa, const uin
  *   wq_dn      E4M3 [E][C][I], sw_dn fp32 [E][C/128][I/128]
  *   out        bf16 or fp32 [T][C] (out_dtype), written in full
  *   workspace  >= fg8_moe_decode_workspace(T, k, C, I) bytes, 16-byte aligned,
- *              whose first FG8_MOE_DECODE_HEAD bytes are zero before the first
- *              call.  A call leaves them ready for the next one of any size; after
- *              one that reported FG8_ERR_TIMEOUT they are to be zeroed again.
+ *              zeroed once, before the first call (its first
+ *              FG8_MOE_DECODE_HEAD bytes hold counters and tagged partial sums).
+ *              A call leaves it ready for the next one of any size; after one that
+ *              reported FG8_ERR_TIMEOUT it is to be zeroed again.
  *              Calls that overlap on the GPU need their own workspace
  *              (FG8_ERR_WORKSPACE_SHARED where that is noticed).
  *   T <= 64, 1 <= k <= min(16, E), E <= 1024, C % 128 == 0, I % 128 == 0;
@@ -524,7 +525,7 @@ fg8_status fg8_grouped_gemm_combine(const uint8_t* a, const float* sa, const uin
  *   A cooperative launch (one CTA per SM); every wait is bounded
  *   (FG8_ERR_TIMEOUT in *dev_status).
  */
-#define FG8_MOE_DECODE_HEAD 4096
+#define FG8_MOE_DECODE_HEAD (4096 + 2 * 160 * 64 * 128 * 8)
 size_t fg8_moe_decode_workspace(int64_t T, int k, int64_t C, int64_t I);
 fg8_status fg8_moe_decode(const uint16_t* x, int64_t T, int C, const float* logits,
                           const float* bias, int32_t* topk_ids, float* affinity, int k, int E,
