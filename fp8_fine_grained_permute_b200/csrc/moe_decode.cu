@@ -184,6 +184,15 @@ FG8_DEV void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) {
         : "memory");
 }
 
+// mbar_wait with what follows a failed first try out of line: every wait of this
+// kernel is code that some CTA meets cold
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag, int32_t* status) {
+    return mbar_wait(bar, parity, abort_flag, status);
+}
+FG8_DEV bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag, int32_t* status) {
+    return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort_flag, status);
+}
+
 FG8_DEV void red_release_gpu(uint32_t* p, uint32_t v) {
     asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
@@ -529,7 +538,7 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
         if (lane == 0) {
             // -------------------------------------------- weight producer
             uint32_t stage = 0, phase = 0;
-            auto take = [&]() { return mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, a.status); };
+            auto take = [&]() { return wait_bar(empty_bar(stage), phase ^ 1u, abort_flag, a.status); };
             auto next = [&]() {
                 if (++stage == S) {
                     stage = 0;
@@ -586,8 +595,8 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
             int k2 = cd.d;
 #pragma unroll 1
             for (int n = 0; n < n_all; ++n) {
-                if (!mbar_wait(tempty_bar(buf), bphase ^ 1u, abort_flag, a.status) ||
-                    !mbar_wait(full_bar(stage), phase, abort_flag, a.status))
+                if (!wait_bar(tempty_bar(buf), bphase ^ 1u, abort_flag, a.status) ||
+                    !wait_bar(full_bar(stage), phase, abort_flag, a.status))
                     break;
                 tc_fence_after();
                 const uint32_t sA = sbase + stage * K::kStage, sB = sA + kABytes;
@@ -655,7 +664,7 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
                 mbar_arrive(bar);
             }
             __syncwarp();
-            return mbar_wait(bar, 0, abort_flag, a.status) && !*abort_flag;
+            return wait_bar(bar, 0, abort_flag, a.status) && !*abort_flag;
         };
         // rows of 128 codes, row j at base + stride * index(j): all loads, then,
         // once the stage is free, all stores
@@ -715,7 +724,7 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
                     cb += kFillWarps;
                     advance();
                 }
-                if (!(ok = mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, a.status))) break;
+                if (!(ok = wait_bar(empty_bar(stage), phase ^ 1u, abort_flag, a.status))) break;
                 store_rows(v, smem + stage * K::kStage + kABytes, cnt);
                 publish(fac);
                 next();
@@ -754,7 +763,7 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
                     k2 += kFillWarps;
                     advance();
                 }
-                if (!(ok = mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, a.status))) break;
+                if (!(ok = wait_bar(empty_bar(stage), phase ^ 1u, abort_flag, a.status))) break;
                 uint8_t* B = smem + stage * K::kStage + kABytes;
                 store_rows(v, B, cnt);
                 if (two) store_rows(w, B + N * 128, cnt);
@@ -773,7 +782,7 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
         auto meet = [&]() {
             __syncwarp();
             if (lane == 0) mbar_arrive(group_bar);
-            const bool r = mbar_wait(group_bar, gphase, abort_flag, a.status);
+            const bool r = wait_bar(group_bar, gphase, abort_flag, a.status);
             gphase ^= 1u;
             return __all_sync(kFull, r) != 0;
         };
@@ -781,7 +790,7 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
         // acc[i] += partial[i] * factor[i] for one step's 2 N columns (the first
         // half only where the step has one K block)
         auto promote = [&](bool two) {
-            if (!__all_sync(kFull, mbar_wait(tfull_bar(buf), bphase, abort_flag, a.status))) return false;
+            if (!__all_sync(kFull, wait_bar(tfull_bar(buf), bphase, abort_flag, a.status))) return false;
             tc_fence_after();
             const float4* f4 = reinterpret_cast<const float4*>(s_factors + slot * 2 * N);
 #pragma unroll
