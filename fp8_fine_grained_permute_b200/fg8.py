@@ -367,25 +367,51 @@ def _u16(x: torch.Tensor) -> torch.Tensor:
     raise TypeError("expected bf16 data")
 
 
-def _out(t, shape, dtype, device):
-    """The caller's output tensor, checked, or a new one."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+def _bf16(x):
+    """bf16 data as it is (or its bit patterns): only the type is checked."""
+    if x.dtype is not torch.bfloat16 and x.dtype not in (torch.int16, torch.uint16):
+        raise TypeError("expected bf16 data")
+    return x
+
+
+def _here(t):
+    """The launch goes to the current device: refuse tensors of another one."""
+    if t.is_cuda and t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"tensors on {t.device}, current device cuda:{torch.cuda.current_device()}")
+
+
+def _raw(t):
+    """A tensor's pointer, or the tensor itself where it is not one the library
+    takes (_call then says so, after all shapes and types were looked at)."""
+    return None if t is None else t.data_ptr() if t.is_cuda and t.is_contiguous() else t
+
+
+def _arg(what, t, shape, dtype):
+    """_raw of a tensor that has to have this shape and type (one pass a tensor: a
+    helper's checks cost host time on every call)."""
     if t.shape != shape or t.dtype is not dtype:
-        raise ValueError(f"output of shape {tuple(t.shape)} {t.dtype}, expected {tuple(shape)} {dtype}")
-    return t
-
-
-def _want(what, t, shape, dtype):
-    """Check an input tensor that a helper derives no size from."""
-    if t is not None and (t.shape != shape or t.dtype is not dtype):
         raise ValueError(f"{what} of shape {tuple(t.shape)} {t.dtype}, expected {tuple(shape)} {dtype}")
+    return t.data_ptr() if t.is_cuda and t.is_contiguous() else t
 
 
-def _want_n(what, t, n, dtype):
-    """As _want, for a tensor of n elements of any shape."""
+def _arg_n(what, t, n, dtype):
+    """As _arg, for a tensor of n elements of any shape."""
     if t.numel() != n or t.dtype is not dtype:
         raise ValueError(f"{what} of {t.numel()} {t.dtype}, expected {n} {dtype}")
+    return t.data_ptr() if t.is_cuda and t.is_contiguous() else t
+
+
+def _call(name, stream, *args):
+    """Call an entry point of the library with _arg results and the stream."""
+    try:
+        status = getattr(lib(), name)(*args, _stream(stream))
+    except (ctypes.ArgumentError, RuntimeError):   # a tensor among them, or no GPU at all
+        for a in args:
+            if isinstance(a, torch.Tensor):
+                _ptr(a)   # raises
+        raise
+    if status != FG8_OK:
+        raise FG8Error(status, name)
 
 
 def new_status(device=None) -> torch.Tensor:
@@ -545,20 +571,21 @@ def grouped_gemm_swiglu_quant_save(a, sa, b, sb, offsets, hq=None, sh=None, guq=
                                    dev_status=None, stream=None):
     """As grouped_gemm_swiglu_quant, keeping the gate and up projections in 8 bits
     for the backward: -> (hq [M, I] u8, sh [I/128, M], guq [M, 2I] u8, sgu [2I/128, M])."""
-    M_total, K = a.shape
-    E, I = offsets.numel() - 1, b.shape[1] // 2
-    dev = a.device
-    _want("a", a, (M_total, K), torch.uint8)
-    _want("sa", sa, (K // 128, M_total), torch.float32)
-    _want("b", b, (E, 2 * I, K), torch.uint8)
-    _want("sb", sb, (E, 2 * I // 128, K // 128), torch.float32)
-    _want("offsets", offsets, (E + 1,), torch.int32)
-    hq = _out(hq, (M_total, I), torch.uint8, dev)
-    sh = _out(sh, (I // 128, M_total), torch.float32, dev)
-    guq = _out(guq, (M_total, 2 * I), torch.uint8, dev)
-    sgu = _out(sgu, (2 * I // 128, M_total), torch.float32, dev)
-    fg8_grouped_gemm_swiglu_quant_save(a, sa, b, sb, offsets, M_total, I, K, E, hq, sh, guq, sgu,
-                                       dev_status, stream)
+    M, K = a.shape
+    E, I, dev = offsets.numel() - 1, b.shape[1] // 2, a.device
+    u8, f32 = torch.uint8, torch.float32
+    _here(a)
+    hq = torch.empty((M, I), dtype=u8, device=dev) if hq is None else hq
+    sh = torch.empty((I // 128, M), dtype=f32, device=dev) if sh is None else sh
+    guq = torch.empty((M, 2 * I), dtype=u8, device=dev) if guq is None else guq
+    sgu = torch.empty((2 * I // 128, M), dtype=f32, device=dev) if sgu is None else sgu
+    _call("fg8_grouped_gemm_swiglu_quant_save", stream,
+        _arg("a", a, (M, K), u8), _arg("sa", sa, (K // 128, M), f32),
+        _arg("b", b, (E, 2 * I, K), u8), _arg("sb", sb, (E, 2 * I // 128, K // 128), f32),
+        _arg("offsets", offsets, (E + 1,), torch.int32), M, I, K, E,
+        _arg("hq", hq, (M, I), u8), _arg("sh", sh, (I // 128, M), f32),
+        _arg("guq", guq, (M, 2 * I), u8), _arg("sgu", sgu, (2 * I // 128, M), f32),
+        _raw(dev_status))
     return hq, sh, guq, sgu
 
 
@@ -572,20 +599,28 @@ def swiglu_backward_quant(dh, guq, sgu, offsets, row_w=None, dq=None, sd=None, d
     R, I = dh.shape
     E, dev = offsets.numel() - 1, dh.device
     P = fg8_colwise_capacity(R, E)
-    u8, f32 = torch.uint8, torch.float32
-    _want("guq", guq, (R, 2 * I), u8)
-    _want("sgu", sgu, (2 * I // 128, R), f32)
-    _want("offsets", offsets, (E + 1,), torch.int32)
-    _want("row_w", row_w, (R,), f32)
-    o = dict(dq=_out(dq, (R, 2 * I), u8, dev), sd=_out(sd, (2 * I // 128, R), f32, dev),
-             dqT=_out(dqT, (2 * I, P), u8, dev), sdT=_out(sdT, (P // 128, 2 * I), f32, dev),
-             hqT=_out(hqT, (I, P), u8, dev), shT=_out(shT, (P // 128, I), f32, dev),
-             gate_dot=_out(gate_dot, (I // 128, R), f32, dev),
-             offsets_out=_out(offsets_out, (E + 1,), torch.int32, dev))
-    fg8_swiglu_backward_quant(_u16(dh), guq, sgu, row_w, offsets, R, I, E, o["dq"], o["sd"],
-                              o["dqT"], o["sdT"], o["hqT"], o["shT"], o["gate_dot"],
-                              o["offsets_out"], dev_status, stream)
-    return o
+    u8, f32, i32 = torch.uint8, torch.float32, torch.int32
+    _here(dh)
+    new = torch.empty
+    dq = new((R, 2 * I), dtype=u8, device=dev) if dq is None else dq
+    sd = new((2 * I // 128, R), dtype=f32, device=dev) if sd is None else sd
+    dqT = new((2 * I, P), dtype=u8, device=dev) if dqT is None else dqT
+    sdT = new((P // 128, 2 * I), dtype=f32, device=dev) if sdT is None else sdT
+    hqT = new((I, P), dtype=u8, device=dev) if hqT is None else hqT
+    shT = new((P // 128, I), dtype=f32, device=dev) if shT is None else shT
+    gate_dot = new((I // 128, R), dtype=f32, device=dev) if gate_dot is None else gate_dot
+    offsets_out = new((E + 1,), dtype=i32, device=dev) if offsets_out is None else offsets_out
+    _call("fg8_swiglu_backward_quant", stream,
+        _raw(_bf16(dh)), _arg("guq", guq, (R, 2 * I), u8), _arg("sgu", sgu, (2 * I // 128, R), f32),
+        None if row_w is None else _arg("row_w", row_w, (R,), f32),
+        _arg("offsets", offsets, (E + 1,), i32), R, I, E,
+        _arg("dq", dq, (R, 2 * I), u8), _arg("sd", sd, (2 * I // 128, R), f32),
+        _arg("dqT", dqT, (2 * I, P), u8), _arg("sdT", sdT, (P // 128, 2 * I), f32),
+        _arg("hqT", hqT, (I, P), u8), _arg("shT", shT, (P // 128, I), f32),
+        _arg("gate_dot", gate_dot, (I // 128, R), f32),
+        _arg("offsets_out", offsets_out, (E + 1,), i32), _raw(dev_status))
+    return dict(dq=dq, sd=sd, dqT=dqT, sdT=sdT, hqT=hqT, shT=shT, gate_dot=gate_dot,
+                offsets_out=offsets_out)
 
 
 def requantize_colwise(xq, sx, offsets, row_token=None, xqT=None, saT=None, offsets_out=None,
@@ -596,15 +631,17 @@ def requantize_colwise(xq, sx, offsets, row_token=None, xqT=None, saT=None, offs
     R = T if row_token is None else row_token.numel()
     E, dev = offsets.numel() - 1, xq.device
     P = fg8_colwise_capacity(R, E)
-    _want("xq", xq, (T, K), torch.uint8)
-    _want("sx", sx, (K // 128, T), torch.float32)
-    _want("offsets", offsets, (E + 1,), torch.int32)
-    _want("row_token", row_token, (R,), torch.int32)
-    xqT = _out(xqT, (K, P), torch.uint8, dev)
-    saT = _out(saT, (P // 128, K), torch.float32, dev)
-    offsets_out = _out(offsets_out, (E + 1,), torch.int32, dev)
-    fg8_requantize_colwise(xq, sx, T, K, row_token, offsets, R, E, xqT, saT, offsets_out,
-                           dev_status, stream)
+    u8, f32, i32 = torch.uint8, torch.float32, torch.int32
+    _here(xq)
+    xqT = torch.empty((K, P), dtype=u8, device=dev) if xqT is None else xqT
+    saT = torch.empty((P // 128, K), dtype=f32, device=dev) if saT is None else saT
+    offsets_out = torch.empty((E + 1,), dtype=i32, device=dev) if offsets_out is None else offsets_out
+    _call("fg8_requantize_colwise", stream,
+        _arg("xq", xq, (T, K), u8), _arg("sx", sx, (K // 128, T), f32), T, K,
+        None if row_token is None else _arg("row_token", row_token, (R,), i32),
+        _arg("offsets", offsets, (E + 1,), i32), R, E, _arg("xqT", xqT, (K, P), u8),
+        _arg("saT", saT, (P // 128, K), f32), _arg("offsets_out", offsets_out, (E + 1,), i32),
+        _raw(dev_status))
     return xqT, saT, offsets_out
 
 
@@ -612,12 +649,12 @@ def gate_weights(token_row, affinity, R, normalize=True, row_w=None, stream=None
     """token_row int32 [T*k], affinity fp32 [T, k] -> row_w fp32 [R]: the combine's
     gate weight of every routed row (0 where no slot names the row)."""
     T, k = affinity.shape
-    _want_n("token_row", token_row, T * k, torch.int32)
-    _want("affinity", affinity, (T, k), torch.float32)
-    if row_w is None:
-        row_w = torch.zeros(R, dtype=torch.float32, device=affinity.device)
-    _want("row_w", row_w, (R,), torch.float32)
-    fg8_gate_weights(token_row, affinity, T, k, int(bool(normalize)), R, row_w, stream)
+    f32 = torch.float32
+    _here(affinity)
+    row_w = torch.zeros(R, dtype=f32, device=affinity.device) if row_w is None else row_w
+    _call("fg8_gate_weights", stream, _arg_n("token_row", token_row, T * k, torch.int32),
+                                  _arg("affinity", affinity, (T, k), f32), T, k,
+                                  int(bool(normalize)), R, _arg("row_w", row_w, (R,), f32))
     return row_w
 
 
@@ -627,14 +664,16 @@ def gate_backward(gate_dot, token_row, topk_ids, affinity, E, normalize=True, da
     dlogits [T, E]): the gradients of the chosen affinities and router logits."""
     nb, R = gate_dot.shape
     T, k = affinity.shape
-    _want("gate_dot", gate_dot, (nb, R), torch.float32)
-    _want_n("token_row", token_row, T * k, torch.int32)
-    _want_n("topk_ids", topk_ids, T * k, torch.int32)
-    _want("affinity", affinity, (T, k), torch.float32)
-    daffinity = _out(daffinity, (T, k), torch.float32, affinity.device)
-    dlogits = _out(dlogits, (T, E), torch.float32, affinity.device)
-    fg8_gate_backward(gate_dot, nb, R, token_row, topk_ids, affinity, T, k, E,
-                      int(bool(normalize)), daffinity, dlogits, stream)
+    f32, i32, dev = torch.float32, torch.int32, affinity.device
+    _here(affinity)
+    daffinity = torch.empty((T, k), dtype=f32, device=dev) if daffinity is None else daffinity
+    dlogits = torch.empty((T, E), dtype=f32, device=dev) if dlogits is None else dlogits
+    _call("fg8_gate_backward", stream, _arg("gate_dot", gate_dot, (nb, R), f32), nb, R,
+                                   _arg_n("token_row", token_row, T * k, i32),
+                                   _arg_n("topk_ids", topk_ids, T * k, i32),
+                                   _arg("affinity", affinity, (T, k), f32), T, k, E,
+                                   int(bool(normalize)), _arg("daffinity", daffinity, (T, k), f32),
+                                   _arg("dlogits", dlogits, (T, E), f32))
     return daffinity, dlogits
 
 
@@ -675,25 +714,26 @@ def moe_decode(x, wq_up, sw_up, wq_dn, sw_dn, k, logits=None, bias=None, ids=Non
     [T, E] and bias [E] (routing included; ids and affinity are then outputs) or
     ids int32 [T, k] and affinity fp32 [T, k] -> (out [T, C], ids, affinity)."""
     T, C = x.shape
-    E, I = wq_up.shape[0], wq_dn.shape[2]
-    dev = x.device
-    f32, u8 = torch.float32, torch.uint8
-    _want("wq_up", wq_up, (E, 2 * I, C), u8)
-    _want("sw_up", sw_up, (E, 2 * I // 128, C // 128), f32)
-    _want("wq_dn", wq_dn, (E, C, I), u8)
-    _want("sw_dn", sw_dn, (E, C // 128, I // 128), f32)
-    _want("logits", logits, (T, E), f32)
-    _want("bias", bias, (E,), f32)
+    E, I, dev = wq_up.shape[0], wq_dn.shape[2], x.device
+    f32, u8, i32 = torch.float32, torch.uint8, torch.int32
+    _here(x)
     if logits is None and (ids is None or affinity is None):
         raise ValueError("moe_decode needs logits and bias, or ids and affinity")
-    ids = _out(ids, (T, k), torch.int32, dev)
-    affinity = _out(affinity, (T, k), f32, dev)
-    out = _out(out, (T, C), f32 if out_dtype == FG8_OUT_F32 else torch.bfloat16, dev)
+    out_t = f32 if out_dtype == FG8_OUT_F32 else torch.bfloat16
+    ids = torch.empty((T, k), dtype=i32, device=dev) if ids is None else ids
+    affinity = torch.empty((T, k), dtype=f32, device=dev) if affinity is None else affinity
+    out = torch.empty((T, C), dtype=out_t, device=dev) if out is None else out
     if workspace is None and T > 0:
         workspace = moe_decode_workspace(T, k, C, I, dev)
-    fg8_moe_decode(_u16(x), T, C, logits, bias, ids, affinity, k, E, wq_up, sw_up, I, wq_dn, sw_dn,
-                   int(bool(normalize)), out_dtype, out, workspace,
-                   0 if workspace is None else workspace.numel(), dev_status, stream)
+    _call("fg8_moe_decode", stream,
+        _raw(_bf16(x)), T, C, None if logits is None else _arg("logits", logits, (T, E), f32),
+        None if logits is None else _arg("bias", bias, (E,), f32), _arg("ids", ids, (T, k), i32),
+        _arg("affinity", affinity, (T, k), f32), k, E, _arg("wq_up", wq_up, (E, 2 * I, C), u8),
+        _arg("sw_up", sw_up, (E, 2 * I // 128, C // 128), f32), I,
+        _arg("wq_dn", wq_dn, (E, C, I), u8),
+        _arg("sw_dn", sw_dn, (E, C // 128, I // 128), f32), int(bool(normalize)), out_dtype,
+        _arg("out", out, (T, C), out_t), _raw(workspace),
+        0 if workspace is None else workspace.numel(), _raw(dev_status))
     return out, ids, affinity
 
 
