@@ -183,7 +183,7 @@ act_backward(const __grid_constant__ CUtensorMap tm_dh, const __grid_constant__ 
         }
         const float4* fac = reinterpret_cast<const float4*>(s_scales + 512 * st);
         const uint8_t* sdh = smem + st * kStage + 8 * lane;
-        const uint8_t* sg = smem + st * kStage + kDhBytes + 4 * lane;
+        const uint32_t a_g = sbase + st * kStage + kDhBytes + 4 * lane;   // gate codes; up codes kCodeBytes further on
         const int r0 = kRows * warp;
         ok = mbar_wait(full_bar(st), (n >> 1) & 1, abort_flag, a.status);
 
@@ -223,16 +223,14 @@ act_backward(const __grid_constant__ CUtensorMap tm_dh, const __grid_constant__ 
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int r = r0 + i + h;
-                    const uint32_t gw = *reinterpret_cast<const uint32_t*>(sg + r * 128);
-                    const uint32_t uw = *reinterpret_cast<const uint32_t*>(sg + kCodeBytes + r * 128);
                     const uint2 dw = *reinterpret_cast<const uint2*>(sdh + r * 256);
                     const float4 f4 = fac[r];
                     const float2 fg = splat(f4.x), fu = splat(f4.y), w = splat(f4.z);
                     float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int p = 0; p < 2; ++p) {
-                        const float2 g = __fmul2_rn(fg8::e4m3x2_f32(p ? gw >> 16 : gw & 0xFFFFu), fg);
-                        const float2 u = __fmul2_rn(fg8::e4m3x2_f32(p ? uw >> 16 : uw & 0xFFFFu), fu);
+                        const float2 g = __fmul2_rn(fg8::e4m3x2_at(a_g + r * 128 + 2 * p), fg);
+                        const float2 u = __fmul2_rn(fg8::e4m3x2_at(a_g + kCodeBytes + r * 128 + 2 * p), fu);
                         const uint32_t db = p ? dw.y : dw.x;
                         const float2 dh = make_float2(fg8::bf16_lo(db), fg8::bf16_hi(db));
                         // exp overflows to infinity for very negative gates: sig is 0 then
@@ -370,10 +368,10 @@ act_backward(const __grid_constant__ CUtensorMap tm_dh, const __grid_constant__ 
                 by_columns(v, 1);
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
-                    const uint32_t uw = *reinterpret_cast<const uint32_t*>(sg + kCodeBytes + (r0 + i + h) * 128);
+                    const uint32_t a_u = a_g + kCodeBytes + (r0 + i + h) * 128;
                     const float2 fu = splat(fac[r0 + i + h].y);
-                    v[h][0] = __fmul2_rn(__fmul2_rn(fg8::e4m3x2_f32(uw & 0xFFFFu), fu), S[i + h][0]);
-                    v[h][1] = __fmul2_rn(__fmul2_rn(fg8::e4m3x2_f32(uw >> 16), fu), S[i + h][1]);
+                    v[h][0] = __fmul2_rn(__fmul2_rn(fg8::e4m3x2_at(a_u), fu), S[i + h][0]);
+                    v[h][1] = __fmul2_rn(__fmul2_rn(fg8::e4m3x2_at(a_u + 2), fu), S[i + h][1]);
                 }
                 by_columns(v, 2);
             };

@@ -32,6 +32,23 @@ FG8_DEV void e4m3x4_f32(uint32_t codes, float2& lo, float2& hi) {
     hi = __half22float2(*reinterpret_cast<const __half2*>(&b));
 }
 
+// Two E4M3 codes in shared memory -> fp32.  A 16-bit load hands the conversion its
+// operand as it is; taking a word apart costs two instructions of the pipe (ALU,
+// with the conversions, maxima and byte permutes) that bounds these kernels.
+FG8_DEV float2 e4m3x2_at(uint32_t addr) {
+    uint32_t h;
+    asm volatile(
+        "{\n"
+        ".reg .b16 c;\n"
+        "ld.shared.b16 c, [%1];\n"
+        "cvt.rn.f16x2.e4m3x2 %0, c;\n"
+        "}\n"
+        : "=r"(h)
+        : "r"(addr)
+        : "memory");
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
 // The scale of a tile of fp32 values without the division routine: q = amax /
 // 448 from the rounded reciprocal and one residual correction, the IEEE quotient
 // for every amax >= 2^-110 (checked over all of them); below that the division.

@@ -53,21 +53,6 @@ struct Args {
     int32_t* status;
 };
 
-// Two E4M3 codes in shared memory -> fp32 (a 16-bit load hands the conversion its
-// operand as it is; taking a word apart costs two instructions of the pipe that
-// bounds this kernel).
-FG8_DEV float2 e4m3x2_at(uint32_t addr) {
-    uint32_t h;
-    asm volatile(
-        "{\n"
-        ".reg .b16 c;\n"
-        "ld.shared.b16 c, [%1];\n"
-        "cvt.rn.f16x2.e4m3x2 %0, c;\n"
-        "}\n"
-        : "=r"(h)
-        : "r"(addr));
-    return __half22float2(*reinterpret_cast<const __half2*>(&h));
-}
 // -s by the FMA pipe
 FG8_DEV float negated(float s) {
     float d;
@@ -171,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) requant_columns(const Ar
         float m[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-            const float2 v0 = e4m3x2_at(in_addr + 128 * i), v1 = e4m3x2_at(in_addr + 128 * i + 2);
+            const float2 v0 = fg8::e4m3x2_at(in_addr + 128 * i), v1 = fg8::e4m3x2_at(in_addr + 128 * i + 2);
             const float s = i % 4 == 0 ? sc[i / 4].x : i % 4 == 1 ? sc[i / 4].y : i % 4 == 2 ? sc[i / 4].z : sc[i / 4].w;
             const float ns = negated(s);
             x[i][0] = __fmul2_rn(v0, make_float2(ns, ns));
