@@ -135,7 +135,10 @@ struct Cfg {
 // workspace: a head of counters and the partials of cut units, both at fixed places
 // and never used for anything else, then the codes and scales of x and h.  A word
 // of a partial is {call tag, fp32 value} in 64 bits, so that a reader sees from the
-// word itself that it is this call's: no flag, no fence and no second trip.
+// word itself that it is this call's: no flag, no fence and no second trip.  Tags
+// come round every 2^30 calls; every kClearCalls calls a CTA clears its words, so
+// that none is older than that.
+constexpr uint32_t kClearCalls = 1u << 29;
 constexpr size_t kHeadBytes = 4096;
 struct Head {
     // arrivals are counted over all calls, so nothing is cleared between them
@@ -208,6 +211,12 @@ FG8_DEV uint64_t get_word(const uint64_t* p) {
 }
 FG8_DEV void get_words2(const uint64_t* p, uint64_t& a, uint64_t& b) {   // each of the two as a whole
     asm volatile("ld.relaxed.gpu.global.v2.u64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "l"(p) : "memory");
+}
+// (0 and 3 in the low bits: no tag, so a cleared word is nobody's)
+FG8_DEV uint32_t tag_of(uint32_t call, uint32_t down) { return 4u * call + 1u + down; }
+__device__ __noinline__ void clear_words(uint64_t* p, int n) {   // by the promotion warps
+#pragma unroll 1
+    for (int i = threadIdx.x & 127; i < n; i += 128) p[i] = 0;
 }
 FG8_DEV bool tagged(uint64_t w, uint32_t tag) { return (uint32_t)(w >> 32) == tag; }
 FG8_DEV float value_of(uint64_t w) { return __uint_as_float((uint32_t)w); }
@@ -823,14 +832,18 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
             return a.part + (int64_t)(2 * c + (begin > sh.begin(c) ? 1 : 0)) * kPartWords;
         };
 
-        const uint32_t tag_up = 2u * *s_call, tag_dn = tag_up + 1u;   // never 0
+        const uint32_t tag_up = tag_of(*s_call, 0u), tag_dn = tag_of(*s_call, 1u);
         float* my_acc = s_acc + row;   // this thread's column, its alone
         auto clear = [&]() {
 #pragma unroll
             for (int i = 0; i < 2 * N; ++i) acc[i] = 0.f;
         };
+        if (*s_call % kClearCalls == 0) {
+            clear_words(a.part + (int64_t)2 * cta * kPartWords, 2 * kPartWords);
+            ok = meet();
+        }
         // ---- up-projection
-        if (u0 < u1) {
+        if (ok && u0 < u1) {
             const Share up = plan.up;
             int u = cu.a, cb = cu.b;
             clear();

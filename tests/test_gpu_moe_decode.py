@@ -278,3 +278,26 @@ def test_saturating_inputs():
     assert torch.all(out[2] == 0)
     for t in range(6):
         check(L, x[t:t + 1], ids[t:t + 1], aff[t:t + 1], out[t:t + 1])
+
+
+@pytest.mark.parametrize("calls", [2 ** 29 - 1, 2 ** 30 - 2, 2 ** 31 - 2, 2 ** 32 - 2])
+def test_call_numbers_that_come_round(calls):
+    """The workspace counts calls in 32 bits and tags partial sums with them.  The
+    counters are set as after `calls` calls, and (at a multiple of 2^29, where old
+    words are cleared) every partial to a word that a call 2^30 before left."""
+    L = Layer(8, 1024, 512, 77)
+    x, (lg, bi) = L.x(5), L.routing(5)
+    want = run(L, x, 2, logits=lg, bias=bi)[0]
+    ws = fg8.moe_decode_workspace(5, 2, L.C, L.I)
+    ctas = torch.cuda.get_device_properties(0).multi_processor_count
+    i32 = lambda v: (v + 2 ** 31) % 2 ** 32 - 2 ** 31   # noqa: E731
+    head = ws[:4096].view(torch.int32)
+    head[:2] = i32(calls * ctas)
+    head[2:2 + ctas] = i32(calls)
+    if (calls + 1) % 2 ** 29 == 0:
+        words = ws[4096:4096 + 2 * 160 * 64 * 128 * 8].view(torch.int32).view(2, 160, 64 * 128, 2)
+        words[..., 0] = 0x41200000   # 10.0
+        words[0, ..., 1] = i32(4 * (calls + 2) + 1)
+        words[1, ..., 1] = i32(4 * (calls + 2) + 2)
+    for _ in range(5):
+        assert torch.equal(run(L, x, 2, ws=ws, logits=lg, bias=bi)[0], want)
