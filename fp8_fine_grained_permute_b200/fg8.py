@@ -386,6 +386,15 @@ def _raw(t):
     return None if t is None else t.data_ptr() if t.is_cuda and t.is_contiguous() else t
 
 
+def _zeros(n, dtype, device, stream):
+    """Zeros written on the stream of the call that takes them."""
+    if stream is None:
+        return torch.zeros(n, dtype=dtype, device=device)
+    s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(s):
+        return torch.zeros(n, dtype=dtype, device=device)
+
+
 def _arg(what, t, shape, dtype):
     """_raw of a tensor that has to have this shape and type (one pass a tensor: a
     helper's checks cost host time on every call)."""
@@ -651,7 +660,7 @@ def gate_weights(token_row, affinity, R, normalize=True, row_w=None, stream=None
     T, k = affinity.shape
     f32 = torch.float32
     _here(affinity)
-    row_w = torch.zeros(R, dtype=f32, device=affinity.device) if row_w is None else row_w
+    row_w = _zeros(R, f32, affinity.device, stream) if row_w is None else row_w
     _call("fg8_gate_weights", stream, _arg_n("token_row", token_row, T * k, torch.int32),
                                   _arg("affinity", affinity, (T, k), f32), T, k,
                                   int(bool(normalize)), R, _arg("row_w", row_w, (R,), f32))
@@ -697,13 +706,14 @@ def grouped_gemm_combine(a, sa, b, sb, offsets, row_token, token_row, affinity, 
     return out
 
 
-def moe_decode_workspace(T, k, C, I, device=None):
+def moe_decode_workspace(T, k, C, I, device=None, stream=None):
     """A zeroed workspace for moe_decode calls of up to T tokens (kept by the
-    caller: a call leaves it ready for the next)."""
+    caller: a call leaves it ready for the next).  It is zeroed on `stream` (default:
+    the current one)."""
     n = fg8_moe_decode_workspace(T, k, C, I)
     if n == 0:
         raise ValueError("moe_decode takes 1..64 tokens, 1..16 slots and I >= 128")
-    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+    return _zeros(n, torch.uint8, device or "cuda", stream)
 
 
 def moe_decode(x, wq_up, sw_up, wq_dn, sw_dn, k, logits=None, bias=None, ids=None, affinity=None,
@@ -724,7 +734,7 @@ def moe_decode(x, wq_up, sw_up, wq_dn, sw_dn, k, logits=None, bias=None, ids=Non
     affinity = torch.empty((T, k), dtype=f32, device=dev) if affinity is None else affinity
     out = torch.empty((T, C), dtype=out_t, device=dev) if out is None else out
     if workspace is None and T > 0:
-        workspace = moe_decode_workspace(T, k, C, I, dev)
+        workspace = moe_decode_workspace(T, k, C, I, dev, stream)
     _call("fg8_moe_decode", stream,
         _raw(_bf16(x)), T, C, None if logits is None else _arg("logits", logits, (T, E), f32),
         None if logits is None else _arg("bias", bias, (E,), f32), _arg("ids", ids, (T, k), i32),

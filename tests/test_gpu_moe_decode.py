@@ -301,3 +301,26 @@ def test_call_numbers_that_come_round(calls):
         words[1, ..., 1] = i32(4 * (calls + 2) + 2)
     for _ in range(5):
         assert torch.equal(run(L, x, 2, ws=ws, logits=lg, bias=bi)[0], want)
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_default_workspace_is_zeroed_on_the_given_stream(handle):
+    """The current stream is held up: what the call needs zeroed may not wait in it."""
+    L = Layer(8, 1024, 512, 78)
+    x, (lg, bi) = L.x(4), L.routing(4)
+    want = run(L, x, 2, logits=lg, bias=bi)[0]
+    tr = torch.arange(8, dtype=torch.int32, device="cuda")
+    aff = torch.rand(4, 2, device="cuda")
+    side = torch.cuda.Stream()
+    dirty = torch.full((40 << 20,), 0x5A, dtype=torch.uint8, device="cuda")
+    st = fg8.new_status()
+    torch.cuda.synchronize()
+    del dirty                          # the allocator hands this memory out again
+    torch.cuda._sleep(100_000_000)     # about 50 ms
+    s = side.cuda_stream if handle else side
+    got, _, _ = fg8.moe_decode(x, *L.weights(), 2, logits=lg, bias=bi, dev_status=st, stream=s)
+    w = fg8.gate_weights(tr, aff, 8, normalize=False, stream=s)
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert st.item() == 0 and torch.equal(got, want)
+    assert torch.equal(w, aff.flatten())
