@@ -112,7 +112,7 @@ gate_backward(const float* __restrict__ dot, int nb, int64_t R, const int32_t* _
     if (slot) daff[gt * k + j] = da;
     if (dlogits) {
         __syncwarp();   // the zeros are in place
-        const float v = da * (a * (1.0f - a));
+        const float v = kept ? da * (a * (1.0f - a)) : 0.f;   // a dropped slot's affinity may be anything
         // an expert named by several slots gets their sum, in slot order, from the first of them
         float total = 0.f;
         bool first = true;

@@ -388,7 +388,8 @@ fg8_status fg8_requantize_colwise(const uint8_t* xq, const float* sx, int64_t T,
  * = w[t][j], with w exactly as in fg8_unpermute_combine (the kept affinities
  * summed in fp32 in slot order, one IEEE division when normalize = 1).  Rows
  * that no slot names are not written.
- *   token_row int32 [T*k], affinity fp32 [T][k], row_w fp32 [R]; 1 <= k <= 16
+ *   token_row int32 [T*k], affinity fp32 [T][k], row_w fp32 [R]; 1 <= k <= 16;
+ *   no two slots name the same row
  */
 fg8_status fg8_gate_weights(const int32_t* token_row, const float* affinity, int64_t T, int k,
                             int normalize, int64_t R, float* row_w, fg8_stream_t stream);

@@ -374,6 +374,22 @@ def test_gates_match_formula(T, E, k, nb, normalize):
     assert np.all(got[~hit] == 0)
 
 
+@pytest.mark.parametrize("normalize", [True, False])
+def test_gate_backward_dropped_slots_affinity_may_be_anything(normalize):
+    T, E, k = 5, 7, 3
+    g = torch.Generator(device="cuda").manual_seed(1)
+    aff = torch.rand(T, k, device="cuda", generator=g)
+    ids = torch.tensor([[0, 1, 2], [3, 4, 5], [6, 0, 1], [2, 3, 4], [5, 6, 0]], dtype=torch.int32, device="cuda")
+    tr = torch.arange(T * k, dtype=torch.int32, device="cuda").view(T, k)
+    dot = torch.randn(2, T * k, device="cuda", generator=g)
+    tr[1, 2] = tr[3, 0] = -1
+    aff[1, 2], aff[3, 0] = 0.5, 0.5
+    want = fg8.gate_backward(dot, tr, ids, aff, E, normalize=normalize)
+    aff[1, 2], aff[3, 0] = float("nan"), float("inf")
+    got = fg8.gate_backward(dot, tr, ids, aff, E, normalize=normalize)
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.isfinite(got[1]).all()
+
+
 def test_gate_gradient_against_differences():
     """d/dlogits of L = sum_j w_j D_j with w from the logits, by central differences in 64 bits."""
     rng = np.random.default_rng(2)
