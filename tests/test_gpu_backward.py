@@ -211,6 +211,30 @@ def test_act_backward_garbage_outside_the_experts_rows(oracle):
         assert np.array_equal(a, b), k
 
 
+def test_act_backward_nonfinite_values_of_the_next_expert(oracle):
+    """A tile's rows behind an expert's last belong to the next one: infinities and
+    NaN there change nothing of the first expert's."""
+    counts = [70, 133, 3]
+    c = act_case(counts, 256, seed=18)
+    ref = act_run(c)
+    d = {k: (v.copy() if isinstance(v, np.ndarray) else v.clone() if torch.is_tensor(v) else v) for k, v in c.items()}
+    d["dh"][70:203:2] = float("inf")
+    d["dh"][71:203:3] = float("nan")
+    d["guq"][70:203:5] = 0x7F
+    d["sgu"][:, 72:203] = np.inf
+    d["w"][75:203:4] = np.nan
+    out = act_run(d)
+    for e, (r0, r1) in ((0, (0, 70)), (2, (203, 206))):
+        for k in ("dq", "sd", "gate_dot"):
+            a, b = (ref[k], out[k]) if k == "dq" else (ref[k].T, out[k].T)
+            assert np.array_equal(a[r0:r1], b[r0:r1]), (e, k)
+        p0, p1 = padded(counts)[e], padded(counts)[e + 1]
+        for k in ("dqT", "hqT"):
+            assert np.array_equal(ref[k][:, p0:p1], out[k][:, p0:p1]), (e, k)
+        for k in ("sdT", "shT"):
+            assert np.array_equal(ref[k][p0 // 128:p1 // 128], out[k][p0 // 128:p1 // 128]), (e, k)
+
+
 def test_act_backward_gradient_against_differences(oracle):
     """A central difference of L = sum w dh h along a random direction."""
     c = act_case([150, 20], 128, seed=9)

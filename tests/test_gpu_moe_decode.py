@@ -324,3 +324,26 @@ def test_default_workspace_is_zeroed_on_the_given_stream(handle):
     torch.cuda.synchronize()
     assert st.item() == 0 and torch.equal(got, want)
     assert torch.equal(w, aff.flatten())
+
+
+def test_largest_routing():
+    """64 tokens in 16 slots of 1024 experts, and all their slots on the last expert."""
+    L = Layer(1024, 128, 128, 79)
+    x, (lg, bi) = L.x(64), L.routing(64)
+    out, ids, aff = run(L, x, 16, logits=lg, bias=bi)
+    check(L, x, ids, aff, out)
+    ids = torch.full((64, 16), 1023, dtype=torch.int32, device="cuda")
+    out, _, _ = run(L, x, 16, ids=ids, affinity=aff, out_dtype=fg8.FG8_OUT_F32)
+    check(L, x, ids, aff, out)
+
+
+def test_a_tokens_nan_stays_its_own():
+    L = Layer(6, 384, 256, 80)
+    x, (lg, bi) = L.x(20), L.routing(20)
+    want = run(L, x, 3, logits=lg, bias=bi)[0]
+    x[7, 100] = float("nan")
+    x[13, 3] = float("inf")
+    got = run(L, x, 3, logits=lg, bias=bi)[0]
+    rest = [t for t in range(20) if t not in (7, 13)]
+    assert torch.equal(got[rest], want[rest])
+    assert torch.isnan(got[7]).all() and torch.isnan(got[13]).all()
