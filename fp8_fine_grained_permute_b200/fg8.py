@@ -374,16 +374,24 @@ def _bf16(x):
     return x
 
 
-def _here(t):
-    """The launch goes to the current device: refuse tensors of another one."""
-    if t.is_cuda and t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"tensors on {t.device}, current device cuda:{torch.cuda.current_device()}")
+_device = getattr(torch._C, "_cuda_getDevice", None)   # the current device's number, without a lazy check
+
+
+def _at(t):
+    """A tensor's pointer, or the tensor itself where it is not one the library
+    takes (_call then says so, after all shapes and types were looked at).  The
+    launch goes to the current device: a tensor of another one is refused."""
+    d = t.get_device()
+    if d < 0 or not t.is_contiguous():
+        return t
+    if d != _device():
+        raise ValueError(f"a tensor on cuda:{d}, current device cuda:{_device()}")
+    return t.data_ptr()
 
 
 def _raw(t):
-    """A tensor's pointer, or the tensor itself where it is not one the library
-    takes (_call then says so, after all shapes and types were looked at)."""
-    return None if t is None else t.data_ptr() if t.is_cuda and t.is_contiguous() else t
+    """_at of a tensor that may be left out."""
+    return None if t is None else _at(t)
 
 
 def _zeros(n, dtype, device, stream):
@@ -400,14 +408,14 @@ def _arg(what, t, shape, dtype):
     helper's checks cost host time on every call)."""
     if t.shape != shape or t.dtype is not dtype:
         raise ValueError(f"{what} of shape {tuple(t.shape)} {t.dtype}, expected {tuple(shape)} {dtype}")
-    return t.data_ptr() if t.is_cuda and t.is_contiguous() else t
+    return _at(t)
 
 
 def _arg_n(what, t, n, dtype):
     """As _arg, for a tensor of n elements of any shape."""
     if t.numel() != n or t.dtype is not dtype:
         raise ValueError(f"{what} of {t.numel()} {t.dtype}, expected {n} {dtype}")
-    return t.data_ptr() if t.is_cuda and t.is_contiguous() else t
+    return _at(t)
 
 
 def _call(name, stream, *args):
@@ -583,7 +591,6 @@ def grouped_gemm_swiglu_quant_save(a, sa, b, sb, offsets, hq=None, sh=None, guq=
     M, K = a.shape
     E, I, dev = offsets.numel() - 1, b.shape[1] // 2, a.device
     u8, f32 = torch.uint8, torch.float32
-    _here(a)
     hq = torch.empty((M, I), dtype=u8, device=dev) if hq is None else hq
     sh = torch.empty((I // 128, M), dtype=f32, device=dev) if sh is None else sh
     guq = torch.empty((M, 2 * I), dtype=u8, device=dev) if guq is None else guq
@@ -609,7 +616,6 @@ def swiglu_backward_quant(dh, guq, sgu, offsets, row_w=None, dq=None, sd=None, d
     E, dev = offsets.numel() - 1, dh.device
     P = fg8_colwise_capacity(R, E)
     u8, f32, i32 = torch.uint8, torch.float32, torch.int32
-    _here(dh)
     new = torch.empty
     dq = new((R, 2 * I), dtype=u8, device=dev) if dq is None else dq
     sd = new((2 * I // 128, R), dtype=f32, device=dev) if sd is None else sd
@@ -641,7 +647,6 @@ def requantize_colwise(xq, sx, offsets, row_token=None, xqT=None, saT=None, offs
     E, dev = offsets.numel() - 1, xq.device
     P = fg8_colwise_capacity(R, E)
     u8, f32, i32 = torch.uint8, torch.float32, torch.int32
-    _here(xq)
     xqT = torch.empty((K, P), dtype=u8, device=dev) if xqT is None else xqT
     saT = torch.empty((P // 128, K), dtype=f32, device=dev) if saT is None else saT
     offsets_out = torch.empty((E + 1,), dtype=i32, device=dev) if offsets_out is None else offsets_out
@@ -659,7 +664,6 @@ def gate_weights(token_row, affinity, R, normalize=True, row_w=None, stream=None
     gate weight of every routed row (0 where no slot names the row)."""
     T, k = affinity.shape
     f32 = torch.float32
-    _here(affinity)
     row_w = _zeros(R, f32, affinity.device, stream) if row_w is None else row_w
     _call("fg8_gate_weights", stream, _arg_n("token_row", token_row, T * k, torch.int32),
                                   _arg("affinity", affinity, (T, k), f32), T, k,
@@ -674,7 +678,6 @@ def gate_backward(gate_dot, token_row, topk_ids, affinity, E, normalize=True, da
     nb, R = gate_dot.shape
     T, k = affinity.shape
     f32, i32, dev = torch.float32, torch.int32, affinity.device
-    _here(affinity)
     daffinity = torch.empty((T, k), dtype=f32, device=dev) if daffinity is None else daffinity
     dlogits = torch.empty((T, E), dtype=f32, device=dev) if dlogits is None else dlogits
     _call("fg8_gate_backward", stream, _arg("gate_dot", gate_dot, (nb, R), f32), nb, R,
@@ -726,7 +729,6 @@ def moe_decode(x, wq_up, sw_up, wq_dn, sw_dn, k, logits=None, bias=None, ids=Non
     T, C = x.shape
     E, I, dev = wq_up.shape[0], wq_dn.shape[2], x.device
     f32, u8, i32 = torch.float32, torch.uint8, torch.int32
-    _here(x)
     if logits is None and (ids is None or affinity is None):
         raise ValueError("moe_decode needs logits and bias, or ids and affinity")
     out_t = f32 if out_dtype == FG8_OUT_F32 else torch.bfloat16

@@ -98,3 +98,33 @@ def test_helpers_refuse_cpu_tensors_and_wrong_outputs(L):
                           z(2, 2, dt=torch.float32), 4)
     with pytest.raises(ValueError, match="CUDA"):
         fg8.gate_weights(z(4, dt=torch.int32), z(2, 2, dt=torch.float32), 4)
+
+
+class _Elsewhere:
+    """A tensor of another device, as far as the binding looks at it."""
+    shape, dtype = (4,), torch.float32
+
+    def __init__(self, d, contiguous=True):
+        self.d, self.c = d, contiguous
+
+    def get_device(self):
+        return self.d
+
+    def is_contiguous(self):
+        return self.c
+
+    def numel(self):
+        return 4
+
+    def data_ptr(self):
+        return 4096
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    monkeypatch.setattr(fg8, "_device", lambda: 1)
+    for take in (fg8._raw, lambda t: fg8._arg("x", t, (4,), torch.float32),
+                 lambda t: fg8._arg_n("x", t, 4, torch.float32)):
+        assert take(_Elsewhere(1)) == 4096
+        with pytest.raises(ValueError, match="cuda:0, current device cuda:1"):
+            take(_Elsewhere(0))
+    assert fg8._raw(None) is None
