@@ -469,6 +469,34 @@ def test_up_save_keeps_the_gemms_own_values(oracle, counts, I, K, extra):
     assert torch.all(guq[n:] == CANARY) and torch.all(sgu[:, n:] == -7.0) and torch.all(hq[n:] == CANARY)
 
 
+@pytest.mark.parametrize("lo,hi", [(-64, -58), (-74, -66), (-52, -46)])
+def test_up_save_tiny_and_zero_tiles(lo, hi):
+    """Scales around 2^-100 and below the normal range (the codes' division) and
+    rows of zeros: still the IEEE quotients of the plain GEMM's output."""
+    R, E, K, I = 140, 2, 256, 256
+    gen = torch.Generator().manual_seed(hi)
+    a = W.gen_e4m3_codes((R, K), 1, 5).cuda()
+    a[7] = 0
+    a[139] = 0
+    sa = torch.exp2(torch.empty((K // 128, R)).uniform_(lo, hi, generator=gen)).cuda()
+    b = W.gen_e4m3_codes((E, 2 * I, K), 1, 6).cuda()
+    b[0, :128] = 0
+    sb = torch.exp2(torch.empty((E, 2 * I // 128, K // 128)).uniform_(lo, hi, generator=gen)).cuda()
+    off = torch.from_numpy(offsets_of([100, 40])).cuda()
+    hq, sh, guq, sgu = fg8.grouped_gemm_swiglu_quant_save(a, sa, b, sb, off)
+    hq0, sh0 = fg8.grouped_gemm_swiglu_quant(a, sa, b, sb, off)
+    gu = fg8.grouped_gemm(a, sa, b, sb, off, out_dtype=fg8.FG8_OUT_F32)
+    torch.cuda.synchronize()
+    assert torch.equal(hq, hq0) and torch.equal(sh, sh0)
+    v = gu.cpu().numpy().reshape(R, -1, 128)
+    amax = np.abs(v).max(2)
+    s = np.where(amax == 0, np.float32(1), amax / np.float32(448))
+    s = np.where(s == 0, np.float32(2.0 ** -149), s)
+    z = torch.from_numpy(v / s[..., None]).clamp(-448, 448)
+    assert np.array_equal(sgu.cpu().numpy().T, s)
+    assert np.array_equal(guq.cpu().numpy(), z.to(torch.float8_e4m3fn).view(torch.uint8).numpy().reshape(R, -1))
+
+
 # ---------------------------------------------------------------------------
 # together: one training step of the layer
 # ---------------------------------------------------------------------------
