@@ -9,7 +9,7 @@
 // with its row gather, tiles, padding and outputs.
 //
 // Bytes in and out are 1 an element each (gathered rows come mostly from L2), so
-// the instructions an element decide: conversions run at 32 a cycle and SM
+// the instructions an element decide: conversions to E4M3 run at 32 a cycle and SM
 // against 128 for FMAs.  An element takes one half of a two-wide conversion each
 // way and the quotient as product, residual, correction in packed fp32 (three
 // half instructions; two conversions of a bracket, as the 16-bit quantizers
@@ -24,6 +24,12 @@
 // values in a thread and three shuffles, a thread's codes of a column are 16
 // consecutive bytes, and the 8 lanes of a column write its whole 128-byte line --
 // no exchange through shared memory and one barrier an item.
+//
+// On a B200: 279 us for 8192 token rows x 7168 to 65536 rows of 256 experts (0.55 GB
+// at least, 85 us at the copy rate; 0.64 GB with the padding), 13 us for 333 x 2048
+// to 1998 rows of 64.  The arithmetic alone takes 257 us, the copies alone 188.
+// Columns turned around through shared memory took 346 us; two passes over the staged
+// codes with more CTAs an SM were no faster.
 #include "fg8_columns.cuh"
 #include "fg8_tma.cuh"
 
