@@ -1,5 +1,5 @@
-// fg8_columns.cuh -- pieces of the kernels that quantize down the token axis
-// from 8-bit inputs (act_backward.cu, requant.cu).
+// fg8_columns.cuh -- pieces of the kernels that quantize fp32 values or read 8-bit
+// rows: tile scales, code conversions, and the tiles of the token axis.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -47,6 +47,14 @@ FG8_DEV float2 e4m3x2_at(uint32_t addr) {
         : "r"(addr)
         : "memory");
     return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// tile_scale for tiles of fp32 values: where amax / 448 rounds to 0 (amax below
+// 2^-141, which no tile of 16-bit values reaches) the scale is the smallest
+// positive number, so that no code is a quotient by 0.
+FG8_DEV float tile_scale32(float amax) {
+    const float s = tile_scale(amax);
+    return s == 0.0f ? 1.4e-45f : s;
 }
 
 // The scale of a tile of fp32 values without the division routine: q = amax /

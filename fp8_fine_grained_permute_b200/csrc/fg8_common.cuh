@@ -51,14 +51,6 @@ FG8_DEV float tile_scale(float amax) {
     return amax == 0.0f ? 1.0f : __fdiv_rn(amax, 448.0f);
 }
 
-// tile_scale for tiles of fp32 values: where amax / 448 rounds to 0 (amax below
-// 2^-141, which no tile of 16-bit values reaches) the scale is the smallest
-// positive number, so that no code is a quotient by 0.
-FG8_DEV float tile_scale32(float amax) {
-    const float s = tile_scale(amax);
-    return s == 0.0f ? 1.4e-45f : s;
-}
-
 // Per-tile context of the E4M3 quantization.
 //
 // The exact code of an element is E4M3(z) with z = fp32(x / s) (IEEE
