@@ -166,14 +166,14 @@ TRAFFIC_CAPTURE = {
     "families": {
         "quant_act_permute": (598.5e6, "quant_act", "c5187dc2015d"),
         "quant_weight": (41280.4e6, "quant_weight", "c5689f11fc37"),
-        "gemm_fprop_up_swiglu_quant": (7836.7e6, "gemm", "7d78004fde39"),
+        "gemm_fprop_up_swiglu_quant": (7877.8e6, "gemm", "8a6851172f22"),
         "quant_act_rows": (777.8e6, "quant_act", "c5187dc2015d"),
-        "gemm_fprop_down": (4594.1e6, "gemm", "7d78004fde39"),
-        "gemm_dgrad": (8393.9e6, "gemm", "7d78004fde39"),
+        "gemm_fprop_down": (4594.6e6, "gemm", "8a6851172f22"),
+        "gemm_dgrad": (8363.3e6, "gemm", "8a6851172f22"),
         "quant_act_colwise": (1573.4e6, "quant_act", "c5187dc2015d"),
-        "gemm_wgrad": (31920.1e6, "gemm", "7d78004fde39"),
+        "gemm_wgrad": (31927.9e6, "gemm", "8a6851172f22"),
         "transpose_blockq": (14976.3e6, "transpose", "3f2c2c5f91b7"),
-        "gemm_fprop_up": (8460.5e6, "gemm", "7d78004fde39"),
+        "gemm_fprop_up": (8523.3e6, "gemm", "8a6851172f22"),
         "unpermute_combine": (1044.5e6, "combine", "641810fdcb7b"),
     },
 }
@@ -181,7 +181,7 @@ TRAFFIC_CAPTURE = {
 # the group lists its own headers (the transpose uses none of its device code
 # but one unchanged load helper)
 _SRC = {"quant_act": ["quant_act.cu", "fg8_tma.cuh"], "quant_weight": ["quant_weight.cu", "fg8_tma.cuh"],
-        "transpose": ["transpose_blockq.cu"], "gemm": ["grouped_gemm.cu", "fg8_tma.cuh"],
+        "transpose": ["transpose_blockq.cu"], "gemm": ["grouped_gemm.cu", "fg8_tma.cuh", "fg8_tcgen05.cuh", "fg8_columns.cuh"],
         "combine": ["combine.cu"]}
 _OWN_HEADERS = {"transpose"}
 

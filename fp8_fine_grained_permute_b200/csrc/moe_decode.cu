@@ -44,8 +44,8 @@
 //   256 experts x 7168 x 2048, top 8: 1 token 69 us (0.79), 8 tokens 366 us (0.9 and
 //   more, by the experts met); 64 experts x 2048 x 768, top 6: 1 token 17.4 us (0.25),
 //   37 tokens 72 us (0.64).  The stream runs at HBM speed (a step's 32 KB an SM take
-//   0.68 us, its MMAs 0.6); the rest is the start (2 to 3 us for one token's routing
-//   and lists, up to 8 for 37 tokens), the meeting of all CTAs between the
+//   0.68 us, its MMAs 0.6); the rest is the start (3 us for one token's routing
+//   and lists, 8 for 37 tokens), the meeting of all CTAs between the
 //   projections and the joins.  Measured on the way there: x quantized by every CTA
 //   for itself, flags and fences in the joins, unrolled code (39 us for the first of
 //   the 64-expert cases: instructions that run once are fetched cold).

@@ -28,8 +28,9 @@
 // On a B200: 279 us for 8192 token rows x 7168 to 65536 rows of 256 experts (0.55 GB
 // at least, 85 us at the copy rate; 0.64 GB with the padding), 13 us for 333 x 2048
 // to 1998 rows of 64.  The arithmetic alone takes 257 us, the copies alone 188.
-// Columns turned around through shared memory took 346 us; two passes over the staged
-// codes with more CTAs an SM were no faster.
+// Columns turned around through shared memory took 346 us; threads of 8 tokens, 32
+// warps an SM at 64 registers, 336 us; two passes over the staged codes with more CTAs
+// an SM were no faster.
 #include "fg8_columns.cuh"
 #include "fg8_tma.cuh"
 
