@@ -347,3 +347,29 @@ def test_a_tokens_nan_stays_its_own():
     rest = [t for t in range(20) if t not in (7, 13)]
     assert torch.equal(got[rest], want[rest])
     assert torch.isnan(got[7]).all() and torch.isnan(got[13]).all()
+
+
+@pytest.mark.parametrize("E", [3, 64, 65, 256, 1000])
+def test_routing_is_the_routing_kernels_with_ties_and_masked_experts(E):
+    """Equal scores, experts masked by a bias of -inf, saturated logits: the ids and
+    affinities of the routing kernel, bit for bit."""
+    k = min(E, 7)
+    L = Layer(E, 128, 128, 81)
+    for T in (1, 5, 64):
+        x, (lg, bi) = L.x(T), L.routing(T)
+        lg = (2 * lg).round() / 2      # ties
+        lg[0, 0], lg[-1, -1] = 200.0, -200.0
+        bi = torch.zeros_like(bi)
+        bi[::3] = float("-inf")        # E = 3: fewer finite experts than slots
+        out, ids, aff = run(L, x, k, logits=lg, bias=bi)
+        want = fg8.route_topk(lg, bi, k)
+        assert torch.equal(ids, want[0]) and torch.equal(aff, want[1])
+        check(L, x, ids, aff, out)
+
+
+def test_default_workspace_on_the_default_stream_by_handle():
+    L = Layer(4, 256, 128, 82)
+    x, (lg, bi) = L.x(2), L.routing(2)
+    want = run(L, x, 2, logits=lg, bias=bi)[0]
+    got = run(L, x, 2, logits=lg, bias=bi, stream=torch.cuda.default_stream().cuda_stream)[0]
+    assert torch.equal(got, want)
