@@ -77,6 +77,38 @@ FG8_DEV float inv_scale(float s) {
 }
 FG8_DEV bool scale_subnormal(float s) { return !(s >= 1.17549435e-38f); }
 
+// The code of a quotient x / s without a division: with r = fp32(1 / s) correctly
+// rounded, z0 = fp32(x r) and z = fp32(z0 + fp32(x - z0 s) r), z is the quotient to
+// 2^-46 before its own rounding, so it can differ from the IEEE quotient (by one fp32
+// step) only where x / s lies that close to the middle of two fp32 numbers.  E4M3(z)
+// and E4M3(fp32(x / s)) differ only if those two numbers are a rounding border of
+// E4M3 (a value of at most 5 significant bits) and its neighbour; that leaves the
+// significands of s within 8 units of a multiple of 2^20 and, for each border, a
+// handful of x, and for every one of these (and with a margin) the two lie on the
+// same side of the border (tests/test_corrected_quotient.py).  Scales from kCorrectedMin
+// on keep the residual clear of underflow.  Worked on -1 / s, so that the order of
+// the terms keeps the sign of a zero; the codes' sign bits are turned at the end.
+constexpr float kCorrectedMin = 0x1p-90f;
+struct Corrected {
+    float2 nr, s;
+};
+FG8_DEV Corrected make_corrected(float s) {
+    const float nr = -__frcp_rn(s);
+    return {make_float2(nr, nr), make_float2(s, s)};
+}
+// -x / s
+FG8_DEV float2 negated_quotient(float2 x, const Corrected& q) {
+    const float2 nz = __fmul2_rn(x, q.nr);
+    return __ffma2_rn(__ffma2_rn(nz, q.s, x), q.nr, nz);
+}
+// codes of eight values
+FG8_DEV uint2 quant_corrected(float2 x0, float2 x1, float2 x2, float2 x3, const Corrected& q) {
+    const float2 z0 = negated_quotient(x0, q), z1 = negated_quotient(x1, q);
+    const float2 z2 = negated_quotient(x2, q), z3 = negated_quotient(x3, q);
+    return make_uint2(__byte_perm(cvt_e4m3x2(z0.x, z0.y), cvt_e4m3x2(z1.x, z1.y), 0x5410) ^ 0x80808080u,
+                      __byte_perm(cvt_e4m3x2(z2.x, z2.y), cvt_e4m3x2(z3.x, z3.y), 0x5410) ^ 0x80808080u);
+}
+
 // One 128-row tile of an expert in the padded token axis (tile number `tile`:
 // padded columns from 128 * tile).
 struct RowTile {

@@ -47,7 +47,7 @@
 // the fp32 accumulators -- the 8-bit checkpoint of the activation's inputs --
 // between its half of the exchange and the wait for the other's.  A thread owns a
 // row, so a tile's maximum needs no exchange.  24576 rows of 64 experts, K = 2048,
-// I = 768: 139.6 us with the checkpoint (1.1 PFLOP/s), 123.4 without; with the
+// I = 768: 133 us with the checkpoint (1.16 PFLOP/s), 123.4 without; with the
 // bracketed quantizer, whose redo is a branch for every eight values, and the
 // checkpoint ahead of the exchange it took 148.5.
 //
@@ -822,6 +822,22 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                     }
                     __syncwarp();
                 };
+                // Saving variant: codes by the corrected quotient, branch-free (a bracket's
+                // redo is a branch for every eight values) and with half the conversions;
+                // quant_corrected has the proof that they are the division's.
+                auto save_codes = [&](int first, float sc, uint8_t* base, int64_t pitch) {
+                    if (!__any_sync(0xffffffffu, sc < fg8::kCorrectedMin)) {
+                        const fg8::Corrected cq = fg8::make_corrected(sc);
+                        store_codes64(first, [&](const float2& x0, const float2& x1, const float2& x2, const float2& x3) {
+                            return fg8::quant_corrected(x0, x1, x2, x3, cq);
+                        }, base, pitch);
+                    } else {
+                        const fg8::QScale q = fg8::make_qscale(sc);
+                        store_codes64(first, [&](const float2& x0, const float2& x1, const float2& x2, const float2& x3) {
+                            return fg8::quant8f(x0, x1, x2, x3, q);
+                        }, base, pitch);
+                    }
+                };
                 if (grp == 0)
                     tmem_st64(lb + 64, acc + 32);
                 else
@@ -838,31 +854,8 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                         m4[i & 3] = fmaxf(m4[i & 3], fmaxf(fabsf(acc[i].x), fabsf(acc[i].y)));
                     const float gsc = fg8::tile_scale_fast(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
                     uint8_t* gb = a.gu + (grp ? a.N / 2 : 0) + col0;
-                    if (!__any_sync(0xffffffffu, gsc < 0x1p-100f)) {
-                        // the quotient as product, residual and correction, on -1/s: no
-                        // branch (a bracket's redo is one for every eight values) and half
-                        // the conversions.  Negated, a zero keeps its sign through the sums.
-                        const float nr1 = -__frcp_rn(gsc);
-                        const float2 nr = make_float2(nr1, nr1), s2 = make_float2(gsc, gsc);
-                        auto two = [&](const float2& x) {
-                            const float2 nz = __fmul2_rn(x, nr);
-                            const float2 z = __ffma2_rn(__ffma2_rn(nz, s2, x), nr, nz);
-                            return fg8::cvt_e4m3x2(z.x, z.y);
-                        };
-                        auto fast = [&](const float2& x0, const float2& x1, const float2& x2, const float2& x3) {
-                            return make_uint2(__byte_perm(two(x0), two(x1), 0x5410) ^ 0x80808080u,
-                                              __byte_perm(two(x2), two(x3), 0x5410) ^ 0x80808080u);
-                        };
-                        store_codes64(0, fast, gb, a.N);
-                        store_codes64(32, fast, gb + 64, a.N);
-                    } else {
-                        const fg8::QScale gq = fg8::make_qscale(gsc);
-                        auto exact = [&](const float2& x0, const float2& x1, const float2& x2, const float2& x3) {
-                            return fg8::quant8f(x0, x1, x2, x3, gq);
-                        };
-                        store_codes64(0, exact, gb, a.N);
-                        store_codes64(32, exact, gb + 64, a.N);
-                    }
+                    save_codes(0, gsc, gb, a.N);
+                    save_codes(32, gsc, gb + 64, a.N);
                     if (row_ok)
                         a.gu_scale[(int64_t)((grp ? a.N / 256 : 0) + col0 / 128) * a.M_total + out_row0 + r] = gsc;
                 }
@@ -902,11 +895,16 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                 }
                 amax = fmaxf(amax, s_amax[(grp ^ 1) * BM + r]);
                 const float sc = fg8::tile_scale(amax);
-                const fg8::QScale q = fg8::make_qscale(sc);
                 const int I = a.N / 2;
-                store_codes64(0, [&](const float2& x0, const float2& x1, const float2& x2, const float2& x3) {
-                    return fg8::quant8f(x0, x1, x2, x3, q);
-                }, static_cast<uint8_t*>(a.out) + col0 + 64 * grp, I);
+                uint8_t* const h0 = static_cast<uint8_t*>(a.out) + col0 + 64 * grp;
+                if (kSave) {
+                    save_codes(0, sc, h0, I);
+                } else {
+                    const fg8::QScale q = fg8::make_qscale(sc);
+                    store_codes64(0, [&](const float2& x0, const float2& x1, const float2& x2, const float2& x3) {
+                        return fg8::quant8f(x0, x1, x2, x3, q);
+                    }, h0, I);
+                }
                 if (grp == 0 && row_ok) a.out_scale[(int64_t)(col0 / 128) * a.M_total + out_row0 + r] = sc;
                 tc_fence_before();
                 __syncwarp();

@@ -251,12 +251,12 @@ __device__ __noinline__ bool try_again(uint64_t& t0, volatile int* abort_flag, i
 // residual and correction.  For every pair of a bf16 magnitude and a tile maximum
 // it rounds to the code that the IEEE quotient gives (checked over all mantissas
 // and 30 binades, with reciprocals up to 2 units off), and it takes a tenth of
-// the division's instructions: code size is latency here.  Scales below 2^-100
+// the division's instructions: code size is latency here.  Scales below kCorrectedMin
 // take the division.  The order of the terms keeps the sign of a zero.
 FG8_DEV uint2 quant8_corrected(const uint4& v, float s) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t c[4];
-    if (s >= 0x1p-100f) {
+    if (s >= fg8::kCorrectedMin) {
         const float r = fg8::inv_scale(s);
         const float2 nr = make_float2(-r, -r), s2 = make_float2(s, s);
 #pragma unroll
@@ -277,7 +277,7 @@ FG8_DEV uint2 quant8_corrected(const uint4& v, float s) {
 // One fp32 value over its tile's scale, likewise (to 2^-45 before the rounding).
 FG8_DEV uint32_t code_of(float x, float s) {
     float z;
-    if (s >= 0x1p-100f) {
+    if (s >= fg8::kCorrectedMin) {
         const float r = fg8::inv_scale(s);
         const float z0 = __fmul_rn(x, r);
         z = __fmaf_rn(__fmaf_rn(z0, s, -x), -r, z0);

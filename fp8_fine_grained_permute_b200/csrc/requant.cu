@@ -13,10 +13,10 @@
 // against 128 for FMAs.  An element takes one half of a two-wide conversion each
 // way and the quotient as product, residual, correction in packed fp32 (three
 // half instructions; two conversions of a bracket, as the 16-bit quantizers
-// form, would double the conversions).  With r = fp32(1 / sT) correctly rounded,
-// z0 = x r is off by 2^-23 at most, and z = z0 - (z0 sT - x) r is the quotient
-// to 2^-45 before its own rounding to fp32.  (In that order, on -x and -r, the
-// sign of a zero survives: z0 + (x - z0 sT) r turns -0 into +0.)
+// form, would double the conversions).  It gives the division's codes: see
+// fg8::Corrected.  (Here on -x and -r: z0 - (z0 sT - x) r keeps the sign of a zero,
+// z0 + (x - z0 sT) r turns -0 into +0; turning the codes' sign bits instead, as the
+// saving GEMM does, took 288 us.)
 //
 // CTA = 256 threads, two a SM, with a contiguous range of (128-token tile, 128
 // columns) items each; cp.async gathers two items ahead.  A warp owns 16 columns
@@ -183,9 +183,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) requant_columns(const Ar
         // scale and reciprocal: lane group g works out column g mod 4 and hands it round
         const float mine = group & 2 ? (group & 1 ? m[3] : m[2]) : (group & 1 ? m[1] : m[0]);
         const float s_mine = fg8::tile_scale_fast(mine);
-        // reciprocal 0: the quotient's residual would leave the normal range (scales
-        // below 2^-100), these codes take the division
-        const float r_mine = s_mine >= 0x1p-100f ? -__frcp_rn(s_mine) : 0.f;
+        // reciprocal 0: the quotient's residual would leave the normal range, these
+        // codes take the division
+        const float r_mine = s_mine >= fg8::kCorrectedMin ? -__frcp_rn(s_mine) : 0.f;
         if (group < 4) a.saT[(int64_t)tile * a.K + 128 * cb + col0 + group] = s_mine;
         float s[4], r[4];
 #pragma unroll
