@@ -166,14 +166,14 @@ TRAFFIC_CAPTURE = {
     "families": {
         "quant_act_permute": (598.5e6, "quant_act", "c5187dc2015d"),
         "quant_weight": (41280.4e6, "quant_weight", "c5689f11fc37"),
-        "gemm_fprop_up_swiglu_quant": (7877.8e6, "gemm", "8a6851172f22"),
+        "gemm_fprop_up_swiglu_quant": (8051.9e6, "gemm", "c0082e7e4a78"),
         "quant_act_rows": (777.8e6, "quant_act", "c5187dc2015d"),
-        "gemm_fprop_down": (4594.6e6, "gemm", "8a6851172f22"),
-        "gemm_dgrad": (8363.3e6, "gemm", "8a6851172f22"),
+        "gemm_fprop_down": (4594.3e6, "gemm", "c0082e7e4a78"),
+        "gemm_dgrad": (8419.0e6, "gemm", "c0082e7e4a78"),
         "quant_act_colwise": (1573.4e6, "quant_act", "c5187dc2015d"),
-        "gemm_wgrad": (31927.9e6, "gemm", "8a6851172f22"),
+        "gemm_wgrad": (31927.9e6, "gemm", "c0082e7e4a78"),
         "transpose_blockq": (14976.3e6, "transpose", "3f2c2c5f91b7"),
-        "gemm_fprop_up": (8523.3e6, "gemm", "8a6851172f22"),
+        "gemm_fprop_up": (8555.7e6, "gemm", "c0082e7e4a78"),
         "unpermute_combine": (1044.5e6, "combine", "641810fdcb7b"),
     },
 }
