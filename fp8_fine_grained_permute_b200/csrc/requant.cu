@@ -19,15 +19,17 @@
 // saving GEMM does, took 288 us.)
 //
 // CTA = 256 threads, two a SM, with a contiguous range of (128-token tile, 128
-// columns) items each; cp.async gathers two items ahead.  A warp owns 16 columns
-// of all 128 tokens, a thread 4 columns x 16 tokens: the column maxima are 16
-// values in a thread and three shuffles, a thread's codes of a column are 16
-// consecutive bytes, and the 8 lanes of a column write its whole 128-byte line --
-// no exchange through shared memory and one barrier an item.
+// columns) items each; cp.async gathers three items ahead (two: 280 us, four: 281).
+// A warp owns 16 columns of all 128 tokens, a thread 4 columns x 16 tokens: the
+// column maxima are 16 values in a thread and three shuffles, a thread's codes of a
+// column are 16 consecutive bytes, and the 8 lanes of a column write its whole
+// 128-byte line -- no exchange through shared memory and one barrier an item.
 //
-// On a B200: 279 us for 8192 token rows x 7168 to 65536 rows of 256 experts (0.55 GB
+// On a B200: 271 us for 8192 token rows x 7168 to 65536 rows of 256 experts (0.55 GB
 // at least, 85 us at the copy rate; 0.64 GB with the padding), 13 us for 333 x 2048
-// to 1998 rows of 64.  The arithmetic alone takes 257 us, the copies alone 188.
+// to 1998 rows of 64.  Of 280 us before the fourth stage the arithmetic alone took 257,
+// gathers and stores alone 234 (gathers 66, stores 151: 128-byte lines of as many
+// columns as an item has): both sides of the SM are near their limit at once.
 // Columns turned around through shared memory took 346 us; threads of 8 tokens, 32
 // warps an SM at 64 registers, 336 us; two passes over the staged codes with more CTAs
 // an SM were no faster.
@@ -39,7 +41,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kRows = 16;                            // tokens of a thread
 constexpr int kCtasPerSm = 2;
-constexpr int kStages = 3;
+constexpr int kStages = 4;
 constexpr uint32_t kTile = 128 * 128;                // an item's codes
 constexpr uint32_t kScalePitch = 20;                 // floats from 16 rows' scales to the next 16: conflict-free 16-byte reads
 constexpr uint32_t kOffScale = kStages * kTile;      // float [stages][8][20]
