@@ -725,7 +725,9 @@ def moe_decode(x, wq_up, sw_up, wq_dn, sw_dn, k, logits=None, bias=None, ids=Non
     """The expert layer for a few tokens: x bf16 [T, C], the quantized weights
     (wq_up [E, 2I, C], wq_dn [E, C, I] and their scales) and either logits
     [T, E] and bias [E] (routing included; ids and affinity are then outputs) or
-    ids int32 [T, k] and affinity fp32 [T, k] -> (out [T, C], ids, affinity)."""
+    ids int32 [T, k] and affinity fp32 [T, k] -> (out [T, C], ids, affinity).
+    workspace: moe_decode_workspace(...), kept from call to call (without one each
+    call zeroes its own); calls that overlap on the GPU need their own."""
     T, C = x.shape
     E, I, dev = wq_up.shape[0], wq_dn.shape[2], x.device
     f32, u8, i32 = torch.float32, torch.uint8, torch.int32
