@@ -163,7 +163,7 @@ def _ptr(t):
 
 def _stream(stream) -> int:
     if stream is None:   # the current stream's handle, without building a Stream object
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -377,11 +377,21 @@ def _bf16(x):
 _device = getattr(torch._C, "_cuda_getDevice", None)   # the current device's number, without a lazy check
 
 
-def _at(t):
+def _here():
+    """The current device (-2 without one: no tensor is on it)."""
+    try:
+        return _device()
+    except RuntimeError:
+        return -2
+
+
+def _at(t, here=None):
     """A tensor's pointer, or the tensor itself where it is not one the library
     takes (_call then says so, after all shapes and types were looked at).  The
-    launch goes to the current device: a tensor of another one is refused."""
+    launch goes to the current device (`here`): a tensor of another one is refused."""
     d = t.get_device()
+    if d == here and t.is_contiguous():
+        return t.data_ptr()
     if d < 0 or not t.is_contiguous():
         return t
     if d != _device():
@@ -389,9 +399,9 @@ def _at(t):
     return t.data_ptr()
 
 
-def _raw(t):
+def _raw(t, here=None):
     """_at of a tensor that may be left out."""
-    return None if t is None else _at(t)
+    return None if t is None else _at(t, here)
 
 
 def _zeros(n, dtype, device, stream):
@@ -403,18 +413,22 @@ def _zeros(n, dtype, device, stream):
         return torch.zeros(n, dtype=dtype, device=device)
 
 
-def _arg(what, t, shape, dtype):
+def _arg(what, t, shape, dtype, here=None):
     """_raw of a tensor that has to have this shape and type (one pass a tensor: a
     helper's checks cost host time on every call)."""
     if t.shape != shape or t.dtype is not dtype:
         raise ValueError(f"{what} of shape {tuple(t.shape)} {t.dtype}, expected {tuple(shape)} {dtype}")
+    if t.get_device() == here and t.is_contiguous():
+        return t.data_ptr()
     return _at(t)
 
 
-def _arg_n(what, t, n, dtype):
+def _arg_n(what, t, n, dtype, here=None):
     """As _arg, for a tensor of n elements of any shape."""
     if t.numel() != n or t.dtype is not dtype:
         raise ValueError(f"{what} of {t.numel()} {t.dtype}, expected {n} {dtype}")
+    if t.get_device() == here and t.is_contiguous():
+        return t.data_ptr()
     return _at(t)
 
 
@@ -595,13 +609,14 @@ def grouped_gemm_swiglu_quant_save(a, sa, b, sb, offsets, hq=None, sh=None, guq=
     sh = torch.empty((I // 128, M), dtype=f32, device=dev) if sh is None else sh
     guq = torch.empty((M, 2 * I), dtype=u8, device=dev) if guq is None else guq
     sgu = torch.empty((2 * I // 128, M), dtype=f32, device=dev) if sgu is None else sgu
+    here = _here()
     _call("fg8_grouped_gemm_swiglu_quant_save", stream,
-        _arg("a", a, (M, K), u8), _arg("sa", sa, (K // 128, M), f32),
-        _arg("b", b, (E, 2 * I, K), u8), _arg("sb", sb, (E, 2 * I // 128, K // 128), f32),
-        _arg("offsets", offsets, (E + 1,), torch.int32), M, I, K, E,
-        _arg("hq", hq, (M, I), u8), _arg("sh", sh, (I // 128, M), f32),
-        _arg("guq", guq, (M, 2 * I), u8), _arg("sgu", sgu, (2 * I // 128, M), f32),
-        _raw(dev_status))
+        _arg("a", a, (M, K), u8, here), _arg("sa", sa, (K // 128, M), f32, here),
+        _arg("b", b, (E, 2 * I, K), u8, here), _arg("sb", sb, (E, 2 * I // 128, K // 128), f32, here),
+        _arg("offsets", offsets, (E + 1,), torch.int32, here), M, I, K, E,
+        _arg("hq", hq, (M, I), u8, here), _arg("sh", sh, (I // 128, M), f32, here),
+        _arg("guq", guq, (M, 2 * I), u8, here), _arg("sgu", sgu, (2 * I // 128, M), f32, here),
+        _raw(dev_status, here))
     return hq, sh, guq, sgu
 
 
@@ -625,15 +640,16 @@ def swiglu_backward_quant(dh, guq, sgu, offsets, row_w=None, dq=None, sd=None, d
     shT = new((P // 128, I), dtype=f32, device=dev) if shT is None else shT
     gate_dot = new((I // 128, R), dtype=f32, device=dev) if gate_dot is None else gate_dot
     offsets_out = new((E + 1,), dtype=i32, device=dev) if offsets_out is None else offsets_out
+    here = _here()
     _call("fg8_swiglu_backward_quant", stream,
-        _raw(_bf16(dh)), _arg("guq", guq, (R, 2 * I), u8), _arg("sgu", sgu, (2 * I // 128, R), f32),
-        None if row_w is None else _arg("row_w", row_w, (R,), f32),
-        _arg("offsets", offsets, (E + 1,), i32), R, I, E,
-        _arg("dq", dq, (R, 2 * I), u8), _arg("sd", sd, (2 * I // 128, R), f32),
-        _arg("dqT", dqT, (2 * I, P), u8), _arg("sdT", sdT, (P // 128, 2 * I), f32),
-        _arg("hqT", hqT, (I, P), u8), _arg("shT", shT, (P // 128, I), f32),
-        _arg("gate_dot", gate_dot, (I // 128, R), f32),
-        _arg("offsets_out", offsets_out, (E + 1,), i32), _raw(dev_status))
+        _raw(_bf16(dh), here), _arg("guq", guq, (R, 2 * I), u8, here), _arg("sgu", sgu, (2 * I // 128, R), f32, here),
+        None if row_w is None else _arg("row_w", row_w, (R,), f32, here),
+        _arg("offsets", offsets, (E + 1,), i32, here), R, I, E,
+        _arg("dq", dq, (R, 2 * I), u8, here), _arg("sd", sd, (2 * I // 128, R), f32, here),
+        _arg("dqT", dqT, (2 * I, P), u8, here), _arg("sdT", sdT, (P // 128, 2 * I), f32, here),
+        _arg("hqT", hqT, (I, P), u8, here), _arg("shT", shT, (P // 128, I), f32, here),
+        _arg("gate_dot", gate_dot, (I // 128, R), f32, here),
+        _arg("offsets_out", offsets_out, (E + 1,), i32, here), _raw(dev_status, here))
     return dict(dq=dq, sd=sd, dqT=dqT, sdT=sdT, hqT=hqT, shT=shT, gate_dot=gate_dot,
                 offsets_out=offsets_out)
 
@@ -650,12 +666,13 @@ def requantize_colwise(xq, sx, offsets, row_token=None, xqT=None, saT=None, offs
     xqT = torch.empty((K, P), dtype=u8, device=dev) if xqT is None else xqT
     saT = torch.empty((P // 128, K), dtype=f32, device=dev) if saT is None else saT
     offsets_out = torch.empty((E + 1,), dtype=i32, device=dev) if offsets_out is None else offsets_out
+    here = _here()
     _call("fg8_requantize_colwise", stream,
-        _arg("xq", xq, (T, K), u8), _arg("sx", sx, (K // 128, T), f32), T, K,
-        None if row_token is None else _arg("row_token", row_token, (R,), i32),
-        _arg("offsets", offsets, (E + 1,), i32), R, E, _arg("xqT", xqT, (K, P), u8),
-        _arg("saT", saT, (P // 128, K), f32), _arg("offsets_out", offsets_out, (E + 1,), i32),
-        _raw(dev_status))
+        _arg("xq", xq, (T, K), u8, here), _arg("sx", sx, (K // 128, T), f32, here), T, K,
+        None if row_token is None else _arg("row_token", row_token, (R,), i32, here),
+        _arg("offsets", offsets, (E + 1,), i32, here), R, E, _arg("xqT", xqT, (K, P), u8, here),
+        _arg("saT", saT, (P // 128, K), f32, here), _arg("offsets_out", offsets_out, (E + 1,), i32, here),
+        _raw(dev_status, here))
     return xqT, saT, offsets_out
 
 
@@ -665,9 +682,10 @@ def gate_weights(token_row, affinity, R, normalize=True, row_w=None, stream=None
     T, k = affinity.shape
     f32 = torch.float32
     row_w = _zeros(R, f32, affinity.device, stream) if row_w is None else row_w
-    _call("fg8_gate_weights", stream, _arg_n("token_row", token_row, T * k, torch.int32),
-                                  _arg("affinity", affinity, (T, k), f32), T, k,
-                                  int(bool(normalize)), R, _arg("row_w", row_w, (R,), f32))
+    here = _here()
+    _call("fg8_gate_weights", stream, _arg_n("token_row", token_row, T * k, torch.int32, here),
+                                  _arg("affinity", affinity, (T, k), f32, here), T, k,
+                                  int(bool(normalize)), R, _arg("row_w", row_w, (R,), f32, here))
     return row_w
 
 
@@ -680,12 +698,13 @@ def gate_backward(gate_dot, token_row, topk_ids, affinity, E, normalize=True, da
     f32, i32, dev = torch.float32, torch.int32, affinity.device
     daffinity = torch.empty((T, k), dtype=f32, device=dev) if daffinity is None else daffinity
     dlogits = torch.empty((T, E), dtype=f32, device=dev) if dlogits is None else dlogits
-    _call("fg8_gate_backward", stream, _arg("gate_dot", gate_dot, (nb, R), f32), nb, R,
-                                   _arg_n("token_row", token_row, T * k, i32),
-                                   _arg_n("topk_ids", topk_ids, T * k, i32),
-                                   _arg("affinity", affinity, (T, k), f32), T, k, E,
-                                   int(bool(normalize)), _arg("daffinity", daffinity, (T, k), f32),
-                                   _arg("dlogits", dlogits, (T, E), f32))
+    here = _here()
+    _call("fg8_gate_backward", stream, _arg("gate_dot", gate_dot, (nb, R), f32, here), nb, R,
+                                   _arg_n("token_row", token_row, T * k, i32, here),
+                                   _arg_n("topk_ids", topk_ids, T * k, i32, here),
+                                   _arg("affinity", affinity, (T, k), f32, here), T, k, E,
+                                   int(bool(normalize)), _arg("daffinity", daffinity, (T, k), f32, here),
+                                   _arg("dlogits", dlogits, (T, E), f32, here))
     return daffinity, dlogits
 
 
@@ -739,15 +758,16 @@ def moe_decode(x, wq_up, sw_up, wq_dn, sw_dn, k, logits=None, bias=None, ids=Non
     out = torch.empty((T, C), dtype=out_t, device=dev) if out is None else out
     if workspace is None and T > 0:
         workspace = moe_decode_workspace(T, k, C, I, dev, stream)
+    here = _here()
     _call("fg8_moe_decode", stream,
-        _raw(_bf16(x)), T, C, None if logits is None else _arg("logits", logits, (T, E), f32),
-        None if logits is None else _arg("bias", bias, (E,), f32), _arg("ids", ids, (T, k), i32),
-        _arg("affinity", affinity, (T, k), f32), k, E, _arg("wq_up", wq_up, (E, 2 * I, C), u8),
-        _arg("sw_up", sw_up, (E, 2 * I // 128, C // 128), f32), I,
-        _arg("wq_dn", wq_dn, (E, C, I), u8),
-        _arg("sw_dn", sw_dn, (E, C // 128, I // 128), f32), int(bool(normalize)), out_dtype,
-        _arg("out", out, (T, C), out_t), _raw(workspace),
-        0 if workspace is None else workspace.numel(), _raw(dev_status))
+        _raw(_bf16(x), here), T, C, None if logits is None else _arg("logits", logits, (T, E), f32, here),
+        None if logits is None else _arg("bias", bias, (E,), f32, here), _arg("ids", ids, (T, k), i32, here),
+        _arg("affinity", affinity, (T, k), f32, here), k, E, _arg("wq_up", wq_up, (E, 2 * I, C), u8, here),
+        _arg("sw_up", sw_up, (E, 2 * I // 128, C // 128), f32, here), I,
+        _arg("wq_dn", wq_dn, (E, C, I), u8, here),
+        _arg("sw_dn", sw_dn, (E, C // 128, I // 128), f32, here), int(bool(normalize)), out_dtype,
+        _arg("out", out, (T, C), out_t, here), _raw(workspace, here),
+        0 if workspace is None else workspace.numel(), _raw(dev_status, here))
     return out, ids, affinity
 
 
