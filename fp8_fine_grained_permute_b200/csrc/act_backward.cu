@@ -5,7 +5,7 @@
 // gradient of the activation's output as the down-projection's dgrad of the
 // unweighted output gradient gives it, and w the row's gate weight:
 //     sig = 1 / (1 + exp(-g)),  h = g sig u,  d = w dh
-//     dU = d g sig,   dG = d u sig (1 + g - g sig)
+//     dU = d g sig,   dG = d u sig (1 + g (1 - sig))
 //     gate_dot[block][row] = sum over the 128-column block of dh h  (dL/dw in parts)
 // and the three matrices that the GEMMs of the backward take leave in 8 bits:
 // [dG dU] by rows (dgrad's A), [dG dU] down the token axis per expert (the up
@@ -251,8 +251,9 @@ act_backward(const __grid_constant__ CUtensorMap tm_dh, const __grid_constant__ 
                         const float2 sw = __fmul2_rn(silu, w);
                         dU[h][p] = __fmul2_rn(dh, sw);
                         H[h][p] = __fmul2_rn(u, sw);
-                        // 1 + g (1 - sig)
-                        const float2 f = __ffma2_rn(silu, splat(-1.0f), __fadd2_rn(g, splat(1.0f)));
+                        // 1 + g (1 - sig), in that order: g + 1 - g sig would lose the 1 for
+                        // gates beyond 2^24, where sig is 1 and the difference g - g
+                        const float2 f = __ffma2_rn(g, __ffma2_rn(sig, splat(-1.0f), splat(1.0f)), splat(1.0f));
                         dG[i + h][p] = __fmul2_rn(__fmul2_rn(__fmul2_rn(dh, w), __fmul2_rn(u, sig)), f);
                         S[i + h][p] = sw;
                     }

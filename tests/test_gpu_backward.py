@@ -590,3 +590,44 @@ def test_backward_kernels_in_a_captured_graph_on_a_side_stream(oracle):
         assert np.array_equal(bufs[k].cpu().numpy(), ref[k]), k
     for k in ("dqT", "hqT"):
         assert np.array_equal(bufs[k].cpu().numpy()[:, :used], ref[k][:, :used]), k
+
+
+# ---------------------------------------------------------------------------
+# very large gates
+# ---------------------------------------------------------------------------
+
+def test_act_backward_gates_beyond_the_integers_of_fp32(oracle):
+    """Gates from 2^12 to 2^31 of both signs.  exp(-g) is 0 or infinite there, so sig
+    is 1 or 0 exactly and the last factor of dG, 1 + g (1 - sig), is 1 or meets a sig
+    of 0: nothing grows with g.  For g > 0: dG = d u is off by the roundings of u, d
+    and the three products (5 eps; 8 with the reciprocal of 1), dU = d g and h = g u
+    by those of g, d, u and three products (the same); for g < 0 all are 0."""
+    counts, I = [130, 40], 256
+    c = act_case(counts, I, seed=31)
+    R = c["R"]
+    rng = np.random.default_rng(32)
+    c["guq"][:, :I][(c["guq"][:, :I] & 0x7F) == 0] = 0x01          # no gate of 0
+    c["sgu"][:I // 128] = np.exp2(21 + rng.uniform(0, 1, (I // 128, R))).astype(np.float32)
+    # single values: where g + 1 rounds up, and where it is g
+    c["guq"][:6, :I] = 0x38                                           # code 1.0
+    c["sgu"][:I // 128, :6] = np.float32([2 ** 24, 2 ** 24 + 2, 2 ** 25, 2 ** 23 + 1, 3e9, 2 ** 26 + 8])
+    out = act_run(c)
+    f = act_formula(oracle, c)
+    gu = deq_rows(oracle, c["guq"], c["sgu"])
+    g, u = gu[:, :I], gu[:, I:]
+    assert np.all(np.abs(g) >= 2.0 ** 12) and np.abs(g).max() > 2.0 ** 30
+    # sig < exp(-2^12) < 2^-5900 there (the formula's clip at -700 is not that small):
+    # every product is 0 in fp32, and a tile of zeros has scale 1
+    for key in ("dG", "dU", "wh"):
+        f[key][g < 0] = 0.0
+    tol = lambda v: 8 * EPS * np.abs(v)   # noqa: E731
+    v = np.concatenate([f["dG"], f["dU"]], 1)
+    check_tiles(oracle, out["dq"], out["sd"].T, v, tol(v), "rows")
+    check_columns(oracle, out["dqT"], out["sdT"], v, tol(v), counts, "columns of dG, dU")
+    check_columns(oracle, out["hqT"], out["shT"], f["wh"], tol(f["wh"]), counts, "columns of w h")
+    # the first rows' dG is d u, not 0 and not twice that
+    d = f["dh"] * c["w"].astype(np.float64)[:, None]
+    got = deq_rows(oracle, out["dq"], out["sd"])[:6, :I]
+    du = (d * u)[:6]
+    big = np.abs(du) > 0.1 * np.abs(du).max(1, keepdims=True)
+    assert np.all((np.abs(got - du) <= 2.0 ** -4 * 1.01 * np.abs(du))[big])
