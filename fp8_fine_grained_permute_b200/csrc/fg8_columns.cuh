@@ -59,7 +59,7 @@ FG8_DEV float tile_scale32(float amax) {
 
 // The scale of a tile of fp32 values without the division routine: q = amax /
 // 448 from the rounded reciprocal and one residual correction, the IEEE quotient
-// for every amax >= 2^-110 (checked over all of them); below that the division.
+// for every amax >= 2^-110 (tests/test_corrected_quotient.py); below that the division.
 FG8_DEV float tile_scale_fast(float amax) {
     if (amax < 0x1p-110f) return tile_scale32(amax);
     const float r = 1.0f / 448.0f;

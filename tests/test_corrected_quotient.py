@@ -51,3 +51,62 @@ def test_same_side_of_every_border_as_the_division():
                     assert (z > border) - (z < border) == (q > border) - (q < border), (s, x, m5)
                     pairs += 1
     assert pairs > 20000
+
+
+def _e4m3_key(v):
+    """The code that v rounds to, as its value: nearest, ties to even, saturating."""
+    e = max(v.numerator.bit_length() - v.denominator.bit_length(), -6)
+    while e > -6 and F(2) ** e > v:
+        e -= 1
+    step = F(2) ** (e - 3)
+    n, rest = divmod(v / step, 1)
+    n = int(n) + (rest > F(1, 2) or (rest == F(1, 2) and int(n) % 2 == 1))
+    return min(n * step, F(448))
+
+
+def test_codes_of_16_bit_values_with_reciprocals_up_to_two_units_off():
+    """The few-token layer's input: bf16 values x over s = fp32(amax / 448), with a
+    reciprocal r within two fp32 steps of 1 / s (a hardware reciprocal of one step
+    and a Newton step).  The quotient by product, residual and correction and the
+    IEEE quotient round to the same code, for every mantissa of x and of amax, in
+    every binade of the quotient from its largest down to zero codes (a power of two
+    scales all steps exactly; only the codes' subnormal steps depend on it)."""
+    differ = 0
+    for ma in range(128, 256):
+        s = rn24(F(ma, 448))
+        r0 = rn24(1 / s)
+        ulp = F(1, 2 ** 23)
+        while r0 < ulp * 2 ** 23:
+            ulp /= 2
+        quotients = [(mx, rn24(mx / s)) for mx in range(128, 256)]
+        for d in range(-2, 3):
+            r = r0 + d * ulp
+            for mx, q in quotients:
+                z0 = rn24(mx * r)
+                z = rn24(z0 + rn24(mx - z0 * s) * r)
+                if z == q:
+                    continue
+                differ += 1
+                # one step apart: no border between two codes may lie between them
+                for e in range(-22, 2):
+                    assert _e4m3_key(z * F(2) ** e) == _e4m3_key(q * F(2) ** e), (ma, mx, d, e)
+    assert differ > 0
+
+
+def test_tile_scale_without_division():
+    """amax / 448 from the rounded reciprocal and one residual correction is the IEEE
+    quotient for every mantissa of amax (the residual is exact and clear of underflow
+    for amax >= 2^-110)."""
+    import numpy as np
+    a = np.arange(2 ** 23, 2 ** 24, dtype=np.float64)
+    r = float(np.float32(1) / np.float32(448))
+    f32 = lambda v: v.astype(np.float32).astype(np.float64)   # noqa: E731
+    q = f32(a * r)                        # 48-bit products: exact before the rounding
+    res = f32(a - q * 448.0)              # both exact, and so is their difference
+    p = res * r                           # at most 24 + 24 bits: exact
+    total = q + p
+    # the sum's own rounding to 53 bits must not decide the rounding to 24
+    lost = (q - total) + p
+    low = total.view(np.uint64) & np.uint64(2 ** 29 - 1)
+    assert not np.any((lost != 0) & (low == 2 ** 28))
+    assert np.array_equal(total.astype(np.float32), a.astype(np.float32) / np.float32(448))

@@ -373,3 +373,40 @@ def test_default_workspace_on_the_default_stream_by_handle():
     want = run(L, x, 2, logits=lg, bias=bi)[0]
     got = run(L, x, 2, logits=lg, bias=bi, stream=torch.cuda.default_stream().cuda_stream)[0]
     assert torch.equal(got, want)
+
+
+def test_input_codes_are_the_quantizers_bit_for_bit():
+    """x's codes and scales, in a kept workspace, are those of quantize_act_rows: for
+    tiles of every mantissa of the maximum, values on exact midpoints between two
+    codes, subnormal scales and tiles of zeros."""
+    T, C = 64, 1024
+    L = Layer(2, C, 128, 83)
+    x = L.x(T).float()
+    tiles = x.view(T, C // 128, 128)
+    m = torch.arange(128, device="cuda").float() / 128 + 1          # every bf16 mantissa
+    tiles[:16] *= 0.1
+    tiles[:16, :, 5] = 8.0 * m.view(16, 8)                          # as the tile's maximum, random values below
+    tiles[16:32, :, :] = (m.flip(0) * torch.exp2(-(torch.arange(128, device="cuda") % 17).float()))[None, None]
+    tiles[16:32, :, 0] = 2 * m.view(16, 8)                          # every mantissa over every maximum
+    # scales that are powers of two: all values midpoints (5 significant bits, or halves of the smallest code)
+    mid = (2 * torch.randint(0, 8, (16, 8, 128), generator=L.g, device="cuda") + 17).float()
+    mid *= torch.exp2(torch.randint(-9, 4, (16, 8, 128), generator=L.g, device="cuda").float())
+    low = (torch.randint(0, 8, (16, 8, 128), generator=L.g, device="cuda").float() + 0.5) * 2.0 ** -9
+    tiles[32:48] = torch.where(torch.rand((16, 8, 128), generator=L.g, device="cuda") < 0.8, mid, low)
+    tiles[32:48, :, 77] = 448.0
+    tiles[32:48] *= torch.exp2(torch.randint(-30, 30, (16, 8, 1), generator=L.g, device="cuda").float())
+    tiles[48:56] *= torch.exp2(-110 - 2.0 * torch.arange(8, device="cuda").float())[:, None, None]
+    tiles[56:58] = 0
+    tiles[58] *= 1e30
+    x *= torch.where(torch.rand(x.shape, generator=L.g, device="cuda") < 0.5, -1.0, 1.0)
+    x = x.to(torch.bfloat16)
+    ws = fg8.moe_decode_workspace(T, 2, C, 128)
+    ids = torch.tensor([[0, 1]] * T, dtype=torch.int32, device="cuda")
+    run(L, x, 2, ws=ws, ids=ids, affinity=torch.ones(T, 2, device="cuda"))
+    want_q, want_s = fg8.quantize_act_rows(x)
+    at = fg8.FG8_MOE_DECODE_HEAD
+    got_q = ws[at:at + T * C].view(T, C)
+    at += (T * C + 255) // 256 * 256
+    got_s = ws[at:at + 4 * T * (C // 128)].view(torch.float32).view(T, C // 128)
+    assert torch.equal(got_s.t(), want_s)
+    assert torch.equal(got_q, want_q)
