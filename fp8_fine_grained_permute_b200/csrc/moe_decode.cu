@@ -249,7 +249,7 @@ __device__ __noinline__ bool try_again(uint64_t& t0, volatile int* abort_flag, i
 
 // E4M3 codes of 8 bf16 values over their tile's scale: the quotient as product,
 // residual and correction.  For every pair of a bf16 magnitude and a tile maximum
-// it rounds to the code that the IEEE quotient gives, with reciprocals up to 2 units
+// it is the IEEE quotient, with reciprocals up to 2 units
 // off (all of them in tests/test_corrected_quotient.py), and it takes a tenth of
 // the division's instructions: code size is latency here.  Scales below kCorrectedMin
 // take the division.  The order of the terms keeps the sign of a zero.

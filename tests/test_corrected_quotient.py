@@ -53,25 +53,13 @@ def test_same_side_of_every_border_as_the_division():
     assert pairs > 20000
 
 
-def _e4m3_key(v):
-    """The code that v rounds to, as its value: nearest, ties to even, saturating."""
-    e = max(v.numerator.bit_length() - v.denominator.bit_length(), -6)
-    while e > -6 and F(2) ** e > v:
-        e -= 1
-    step = F(2) ** (e - 3)
-    n, rest = divmod(v / step, 1)
-    n = int(n) + (rest > F(1, 2) or (rest == F(1, 2) and int(n) % 2 == 1))
-    return min(n * step, F(448))
-
-
-def test_codes_of_16_bit_values_with_reciprocals_up_to_two_units_off():
+def test_quotients_of_16_bit_values_with_reciprocals_up_to_two_units_off():
     """The few-token layer's input: bf16 values x over s = fp32(amax / 448), with a
     reciprocal r within two fp32 steps of 1 / s (a hardware reciprocal of one step
-    and a Newton step).  The quotient by product, residual and correction and the
-    IEEE quotient round to the same code, for every mantissa of x and of amax, in
-    every binade of the quotient from its largest down to zero codes (a power of two
-    scales all steps exactly; only the codes' subnormal steps depend on it)."""
-    differ = 0
+    and a Newton step).  The quotient by product, residual and correction is the IEEE
+    quotient for every mantissa of x and of amax.  (Powers of two scale every step
+    exactly where the code is not 0: x > 2^-11 s, s >= 2^-90, so the residual's last
+    bit is at 2^-149 or above.)"""
     for ma in range(128, 256):
         s = rn24(F(ma, 448))
         r0 = rn24(1 / s)
@@ -79,18 +67,10 @@ def test_codes_of_16_bit_values_with_reciprocals_up_to_two_units_off():
         while r0 < ulp * 2 ** 23:
             ulp /= 2
         quotients = [(mx, rn24(mx / s)) for mx in range(128, 256)]
-        for d in range(-2, 3):
-            r = r0 + d * ulp
+        for r in (r0 + d * ulp for d in range(-2, 3)):
             for mx, q in quotients:
                 z0 = rn24(mx * r)
-                z = rn24(z0 + rn24(mx - z0 * s) * r)
-                if z == q:
-                    continue
-                differ += 1
-                # one step apart: no border between two codes may lie between them
-                for e in range(-22, 2):
-                    assert _e4m3_key(z * F(2) ** e) == _e4m3_key(q * F(2) ** e), (ma, mx, d, e)
-    assert differ > 0
+                assert rn24(z0 + rn24(mx - z0 * s) * r) == q, (ma, mx)
 
 
 def test_tile_scale_without_division():
