@@ -9,7 +9,7 @@ Two layers:
   * `fg8_*` functions with the C names and arguments (tensors or None in place
     of pointers), raising FG8Error on a non-OK status;
   * small helpers (`quantize_act`, `quantize_weight`, ...) that allocate the
-    output tensors with torch and call the former.
+    output tensors with torch, on the stream of the call, and call the former.
 """
 
 from __future__ import annotations
@@ -404,13 +404,28 @@ def _raw(t, here=None):
     return None if t is None else _at(t, here)
 
 
-def _zeros(n, dtype, device, stream):
-    """Zeros written on the stream of the call that takes them."""
-    if stream is None:
-        return torch.zeros(n, dtype=dtype, device=device)
-    s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
-    with torch.cuda.stream(s):
-        return torch.zeros(n, dtype=dtype, device=device)
+def _torch_stream(stream):
+    """The torch stream of a stream argument: one already, or one's handle."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    return torch.cuda.ExternalStream(0 if handle == 1 else handle)   # 1: the legacy default stream, as 0
+
+
+def _new(shape, dtype, device, stream, make=None, scratch=False):
+    """A tensor for a call on `stream` (None: the current one), taken from that
+    stream's memory: a block of another stream's may still be in use there.  The
+    current stream, where the caller usually goes on with it, is noted as a user;
+    scratch is dropped at the end of the call and is not."""
+    make = make or torch.empty
+    if stream is None or torch.device(device).type != "cuda":
+        return make(shape, dtype=dtype, device=device)
+    here = torch.cuda.current_stream(device)
+    with torch.cuda.stream(_torch_stream(stream)):
+        t = make(shape, dtype=dtype, device=device)
+    if not scratch:
+        t.record_stream(here)
+    return t
 
 
 def _arg(what, t, shape, dtype, here=None):
@@ -445,8 +460,9 @@ def _call(name, stream, *args):
         raise FG8Error(status, name)
 
 
-def new_status(device=None) -> torch.Tensor:
-    return torch.zeros(1, dtype=torch.int32, device=device or "cuda")
+def new_status(device=None, stream=None) -> torch.Tensor:
+    """A cleared status word (cleared on `stream`, default: the current one)."""
+    return _new(1, torch.int32, device or "cuda", stream, make=torch.zeros)
 
 
 def quantize_act(x: torch.Tensor, topk_ids: torch.Tensor, E: int, dev_status=None,
@@ -457,16 +473,16 @@ def quantize_act(x: torch.Tensor, topk_ids: torch.Tensor, E: int, dev_status=Non
     R = T * k
     dev = x.device
     out = dict(
-        xq=torch.empty((R, K), dtype=torch.uint8, device=dev),
-        sa=torch.empty((K // 128, R), dtype=torch.float32, device=dev),
-        row_token=torch.empty(R, dtype=torch.int32, device=dev),
-        token_row=torch.empty(T * k, dtype=torch.int32, device=dev),
-        offsets=torch.empty(E + 1, dtype=torch.int32, device=dev),
+        xq=_new((R, K), torch.uint8, dev, stream),
+        sa=_new((K // 128, R), torch.float32, dev, stream),
+        row_token=_new(R, torch.int32, dev, stream),
+        token_row=_new(T * k, torch.int32, dev, stream),
+        offsets=_new(E + 1, torch.int32, dev, stream),
     )
     ws_bytes = fg8_quantize_act_workspace(T, k, E)
     if workspace is None:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-    st = dev_status if dev_status is not None else new_status(dev)
+        workspace = _new(ws_bytes, torch.uint8, dev, stream, scratch=True)
+    st = dev_status if dev_status is not None else new_status(dev, stream)
     fg8_quantize_act(_u16(x), T, K, topk_ids, k, E, None, FG8_ROWWISE, out["xq"], out["sa"],
                      out["row_token"], out["token_row"], out["offsets"], None, None, workspace,
                      ws_bytes, st, stream)
@@ -483,18 +499,18 @@ def route_quantize_act(logits: torch.Tensor, bias: torch.Tensor, x: torch.Tensor
     R = T * k
     dev = x.device
     out = dict(
-        ids=torch.empty((T, k), dtype=torch.int32, device=dev),
-        affinity=torch.empty((T, k), dtype=torch.float32, device=dev),
-        xq=torch.empty((R, K), dtype=torch.uint8, device=dev),
-        sa=torch.empty((K // 128, R), dtype=torch.float32, device=dev),
-        row_token=torch.empty(R, dtype=torch.int32, device=dev),
-        token_row=torch.empty(T * k, dtype=torch.int32, device=dev),
-        offsets=torch.empty(E + 1, dtype=torch.int32, device=dev),
+        ids=_new((T, k), torch.int32, dev, stream),
+        affinity=_new((T, k), torch.float32, dev, stream),
+        xq=_new((R, K), torch.uint8, dev, stream),
+        sa=_new((K // 128, R), torch.float32, dev, stream),
+        row_token=_new(R, torch.int32, dev, stream),
+        token_row=_new(T * k, torch.int32, dev, stream),
+        offsets=_new(E + 1, torch.int32, dev, stream),
     )
     ws_bytes = fg8_quantize_act_workspace(T, k, E)
     if workspace is None:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-    st = dev_status if dev_status is not None else new_status(dev)
+        workspace = _new(ws_bytes, torch.uint8, dev, stream, scratch=True)
+    st = dev_status if dev_status is not None else new_status(dev, stream)
     fg8_route_quantize_act(logits, bias, _u16(x), T, K, k, E, out["ids"], out["affinity"],
                            out["xq"], out["sa"], out["row_token"], out["token_row"],
                            out["offsets"], workspace, ws_bytes, st, stream)
@@ -505,8 +521,8 @@ def route_quantize_act(logits: torch.Tensor, bias: torch.Tensor, x: torch.Tensor
 def quantize_act_rows(x: torch.Tensor, stream=None):
     """1x128 quantize of rows already in expert order -> (xq [R,K], sa [K/128,R])."""
     R, K = x.shape
-    xq = torch.empty((R, K), dtype=torch.uint8, device=x.device)
-    sa = torch.empty((K // 128, R), dtype=torch.float32, device=x.device)
+    xq = _new((R, K), torch.uint8, x.device, stream)
+    sa = _new((K // 128, R), torch.float32, x.device, stream)
     fg8_quantize_act(_u16(x), R, K, None, 1, 1, None, FG8_ROWWISE, xq, sa, None, None, None,
                      None, None, None, 0, None, stream)
     return xq, sa
@@ -519,9 +535,9 @@ def quantize_act_colwise(x: torch.Tensor, offsets: torch.Tensor, k: int = 1,
     E = offsets.numel() - 1
     R = T * k
     P = fg8_colwise_capacity(R, E)
-    xqT = torch.empty((C, P), dtype=torch.uint8, device=x.device)
-    saT = torch.empty((P // 128, C), dtype=torch.float32, device=x.device)
-    padoff = torch.empty(E + 1, dtype=torch.int32, device=x.device)
+    xqT = _new((C, P), torch.uint8, x.device, stream)
+    saT = _new((P // 128, C), torch.float32, x.device, stream)
+    padoff = _new(E + 1, torch.int32, x.device, stream)
     fg8_quantize_act(_u16(x), T, C, None, k, E, offsets, FG8_COLWISE, None, None, row_token,
                      None, padoff, xqT, saT, None, 0, None, stream)
     return xqT, saT, padoff
@@ -530,8 +546,8 @@ def quantize_act_colwise(x: torch.Tensor, offsets: torch.Tensor, k: int = 1,
 def quantize_weight(w: torch.Tensor, status=None, stream=None):
     """128x128 block quantize of bf16 w [E,N,K] -> (wq, sw [E,N/128,K/128])."""
     E, N, K = w.shape
-    wq = torch.empty((E, N, K), dtype=torch.uint8, device=w.device)
-    sw = torch.empty((E, N // 128, K // 128), dtype=torch.float32, device=w.device)
+    wq = _new((E, N, K), torch.uint8, w.device, stream)
+    sw = _new((E, N // 128, K // 128), torch.float32, w.device, stream)
     fg8_quantize_weight(_u16(w), E, N, K, wq, sw, status, stream)
     return wq, sw
 
@@ -540,18 +556,18 @@ def quantize_weight_transposed(w: torch.Tensor, status=None, stream=None):
     """128x128 block quantize of bf16 w [E,N,K] plus its block-transposed copy
     -> (wq, sw, wqT [E,K,N], swT [E,K/128,N/128])."""
     E, N, K = w.shape
-    wq = torch.empty((E, N, K), dtype=torch.uint8, device=w.device)
-    sw = torch.empty((E, N // 128, K // 128), dtype=torch.float32, device=w.device)
-    wqT = torch.empty((E, K, N), dtype=torch.uint8, device=w.device)
-    swT = torch.empty((E, K // 128, N // 128), dtype=torch.float32, device=w.device)
+    wq = _new((E, N, K), torch.uint8, w.device, stream)
+    sw = _new((E, N // 128, K // 128), torch.float32, w.device, stream)
+    wqT = _new((E, K, N), torch.uint8, w.device, stream)
+    swT = _new((E, K // 128, N // 128), torch.float32, w.device, stream)
     fg8_quantize_weight_transposed(_u16(w), E, N, K, wq, sw, wqT, swT, status, stream)
     return wq, sw, wqT, swT
 
 
 def transpose_blockq(wq: torch.Tensor, sw: torch.Tensor, stream=None):
     E, N, K = wq.shape
-    wqT = torch.empty((E, K, N), dtype=torch.uint8, device=wq.device)
-    swT = torch.empty((E, K // 128, N // 128), dtype=torch.float32, device=wq.device)
+    wqT = _new((E, K, N), torch.uint8, wq.device, stream)
+    swT = _new((E, K // 128, N // 128), torch.float32, wq.device, stream)
     fg8_transpose_blockq(wq, sw, E, N, K, wqT, swT, stream)
     return wqT, swT
 
@@ -573,10 +589,10 @@ def grouped_gemm(a, sa, b, sb, offsets, out_dtype=FG8_OUT_BF16, group_mode=FG8_G
         bmode = FG8_BSCALE_ROW128
     if out is None:
         dt = torch.float32 if out_dtype == FG8_OUT_F32 else torch.bfloat16
-        out = torch.empty(shape, dtype=dt, device=a.device)
+        out = _new(shape, dt, a.device, stream)
     ws_bytes = fg8_grouped_gemm_workspace(group_mode)
     if workspace is None and ws_bytes:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=a.device)
+        workspace = _new(ws_bytes, torch.uint8, a.device, stream, scratch=True)
     fg8_grouped_gemm(a, sa, b, sb, offsets, M_total, N, K, E, group_mode, bmode, out_dtype, out,
                      workspace, ws_bytes if workspace is not None else 0, dev_status, stream)
     return out
@@ -590,9 +606,9 @@ def grouped_gemm_swiglu_quant(a, sa, b, sb, offsets, dev_status=None, hq=None, s
     E = offsets.numel() - 1
     I = b.shape[1] // 2
     if hq is None:
-        hq = torch.empty((M_total, I), dtype=torch.uint8, device=a.device)
+        hq = _new((M_total, I), torch.uint8, a.device, stream)
     if sh is None:
-        sh = torch.empty((I // 128, M_total), dtype=torch.float32, device=a.device)
+        sh = _new((I // 128, M_total), torch.float32, a.device, stream)
     fg8_grouped_gemm_swiglu_quant(a, sa, b, sb, offsets, M_total, I, K, E, hq, sh, dev_status,
                                   stream)
     return hq, sh
@@ -605,10 +621,10 @@ def grouped_gemm_swiglu_quant_save(a, sa, b, sb, offsets, hq=None, sh=None, guq=
     M, K = a.shape
     E, I, dev = offsets.numel() - 1, b.shape[1] // 2, a.device
     u8, f32 = torch.uint8, torch.float32
-    hq = torch.empty((M, I), dtype=u8, device=dev) if hq is None else hq
-    sh = torch.empty((I // 128, M), dtype=f32, device=dev) if sh is None else sh
-    guq = torch.empty((M, 2 * I), dtype=u8, device=dev) if guq is None else guq
-    sgu = torch.empty((2 * I // 128, M), dtype=f32, device=dev) if sgu is None else sgu
+    hq = _new((M, I), u8, dev, stream) if hq is None else hq
+    sh = _new((I // 128, M), f32, dev, stream) if sh is None else sh
+    guq = _new((M, 2 * I), u8, dev, stream) if guq is None else guq
+    sgu = _new((2 * I // 128, M), f32, dev, stream) if sgu is None else sgu
     here = _here()
     _call("fg8_grouped_gemm_swiglu_quant_save", stream,
         _arg("a", a, (M, K), u8, here), _arg("sa", sa, (K // 128, M), f32, here),
@@ -631,15 +647,14 @@ def swiglu_backward_quant(dh, guq, sgu, offsets, row_w=None, dq=None, sd=None, d
     E, dev = offsets.numel() - 1, dh.device
     P = fg8_colwise_capacity(R, E)
     u8, f32, i32 = torch.uint8, torch.float32, torch.int32
-    new = torch.empty
-    dq = new((R, 2 * I), dtype=u8, device=dev) if dq is None else dq
-    sd = new((2 * I // 128, R), dtype=f32, device=dev) if sd is None else sd
-    dqT = new((2 * I, P), dtype=u8, device=dev) if dqT is None else dqT
-    sdT = new((P // 128, 2 * I), dtype=f32, device=dev) if sdT is None else sdT
-    hqT = new((I, P), dtype=u8, device=dev) if hqT is None else hqT
-    shT = new((P // 128, I), dtype=f32, device=dev) if shT is None else shT
-    gate_dot = new((I // 128, R), dtype=f32, device=dev) if gate_dot is None else gate_dot
-    offsets_out = new((E + 1,), dtype=i32, device=dev) if offsets_out is None else offsets_out
+    dq = _new((R, 2 * I), u8, dev, stream) if dq is None else dq
+    sd = _new((2 * I // 128, R), f32, dev, stream) if sd is None else sd
+    dqT = _new((2 * I, P), u8, dev, stream) if dqT is None else dqT
+    sdT = _new((P // 128, 2 * I), f32, dev, stream) if sdT is None else sdT
+    hqT = _new((I, P), u8, dev, stream) if hqT is None else hqT
+    shT = _new((P // 128, I), f32, dev, stream) if shT is None else shT
+    gate_dot = _new((I // 128, R), f32, dev, stream) if gate_dot is None else gate_dot
+    offsets_out = _new((E + 1,), i32, dev, stream) if offsets_out is None else offsets_out
     here = _here()
     _call("fg8_swiglu_backward_quant", stream,
         _raw(_bf16(dh), here), _arg("guq", guq, (R, 2 * I), u8, here), _arg("sgu", sgu, (2 * I // 128, R), f32, here),
@@ -663,9 +678,9 @@ def requantize_colwise(xq, sx, offsets, row_token=None, xqT=None, saT=None, offs
     E, dev = offsets.numel() - 1, xq.device
     P = fg8_colwise_capacity(R, E)
     u8, f32, i32 = torch.uint8, torch.float32, torch.int32
-    xqT = torch.empty((K, P), dtype=u8, device=dev) if xqT is None else xqT
-    saT = torch.empty((P // 128, K), dtype=f32, device=dev) if saT is None else saT
-    offsets_out = torch.empty((E + 1,), dtype=i32, device=dev) if offsets_out is None else offsets_out
+    xqT = _new((K, P), u8, dev, stream) if xqT is None else xqT
+    saT = _new((P // 128, K), f32, dev, stream) if saT is None else saT
+    offsets_out = _new((E + 1,), i32, dev, stream) if offsets_out is None else offsets_out
     here = _here()
     _call("fg8_requantize_colwise", stream,
         _arg("xq", xq, (T, K), u8, here), _arg("sx", sx, (K // 128, T), f32, here), T, K,
@@ -681,7 +696,7 @@ def gate_weights(token_row, affinity, R, normalize=True, row_w=None, stream=None
     gate weight of every routed row (0 where no slot names the row)."""
     T, k = affinity.shape
     f32 = torch.float32
-    row_w = _zeros(R, f32, affinity.device, stream) if row_w is None else row_w
+    row_w = _new(R, f32, affinity.device, stream, make=torch.zeros) if row_w is None else row_w
     here = _here()
     _call("fg8_gate_weights", stream, _arg_n("token_row", token_row, T * k, torch.int32, here),
                                   _arg("affinity", affinity, (T, k), f32, here), T, k,
@@ -696,8 +711,8 @@ def gate_backward(gate_dot, token_row, topk_ids, affinity, E, normalize=True, da
     nb, R = gate_dot.shape
     T, k = affinity.shape
     f32, i32, dev = torch.float32, torch.int32, affinity.device
-    daffinity = torch.empty((T, k), dtype=f32, device=dev) if daffinity is None else daffinity
-    dlogits = torch.empty((T, E), dtype=f32, device=dev) if dlogits is None else dlogits
+    daffinity = _new((T, k), f32, dev, stream) if daffinity is None else daffinity
+    dlogits = _new((T, E), f32, dev, stream) if dlogits is None else dlogits
     here = _here()
     _call("fg8_gate_backward", stream, _arg("gate_dot", gate_dot, (nb, R), f32, here), nb, R,
                                    _arg_n("token_row", token_row, T * k, i32, here),
@@ -717,11 +732,10 @@ def grouped_gemm_combine(a, sa, b, sb, offsets, row_token, token_row, affinity, 
     T, k = affinity.shape
     dev = a.device
     if out is None:
-        out = torch.empty((T, N), dtype=torch.float32, device=dev)
+        out = _new((T, N), torch.float32, dev, stream)
     if workspace is None:
-        workspace = torch.empty(max(16, fg8_grouped_gemm_combine_workspace(M_total)),
-                                dtype=torch.uint8, device=dev)
-    st = dev_status if dev_status is not None else new_status(dev)
+        workspace = _new(max(16, fg8_grouped_gemm_combine_workspace(M_total)), torch.uint8, dev, stream, scratch=True)
+    st = dev_status if dev_status is not None else new_status(dev, stream)
     fg8_grouped_gemm_combine(a, sa, b, sb, offsets, M_total, N, K, E, row_token, token_row,
                              affinity, T, k, int(bool(normalize)), out, workspace,
                              workspace.numel(), st, stream)
@@ -735,7 +749,7 @@ def moe_decode_workspace(T, k, C, I, device=None, stream=None):
     n = fg8_moe_decode_workspace(T, k, C, I)
     if n == 0:
         raise ValueError("moe_decode takes 1..64 tokens, 1..16 slots and I >= 128")
-    return _zeros(n, torch.uint8, device or "cuda", stream)
+    return _new(n, torch.uint8, device or "cuda", stream, make=torch.zeros)
 
 
 def moe_decode(x, wq_up, sw_up, wq_dn, sw_dn, k, logits=None, bias=None, ids=None, affinity=None,
@@ -753,9 +767,9 @@ def moe_decode(x, wq_up, sw_up, wq_dn, sw_dn, k, logits=None, bias=None, ids=Non
     if logits is None and (ids is None or affinity is None):
         raise ValueError("moe_decode needs logits and bias, or ids and affinity")
     out_t = f32 if out_dtype == FG8_OUT_F32 else torch.bfloat16
-    ids = torch.empty((T, k), dtype=i32, device=dev) if ids is None else ids
-    affinity = torch.empty((T, k), dtype=f32, device=dev) if affinity is None else affinity
-    out = torch.empty((T, C), dtype=out_t, device=dev) if out is None else out
+    ids = _new((T, k), i32, dev, stream) if ids is None else ids
+    affinity = _new((T, k), f32, dev, stream) if affinity is None else affinity
+    out = _new((T, C), out_t, dev, stream) if out is None else out
     if workspace is None and T > 0:
         workspace = moe_decode_workspace(T, k, C, I, dev, stream)
     here = _here()
@@ -779,7 +793,7 @@ def unpermute_combine(y, token_row, affinity, normalize=True, out_dtype=FG8_OUT_
     T, k = affinity.shape
     if out is None:
         dt = torch.float32 if out_dtype == FG8_OUT_F32 else torch.bfloat16
-        out = torch.empty((T, C), dtype=dt, device=affinity.device)
+        out = _new((T, C), dt, affinity.device, stream)
     yv = y.view(torch.int16) if y.dtype == torch.bfloat16 else y
     fg8_unpermute_combine(yv, R, C, token_row, affinity, T, k, int(bool(normalize)), out_dtype,
                           out, stream)
@@ -790,8 +804,8 @@ def route_topk(logits, bias, k, ids=None, affinity=None, stream=None):
     """logits fp32 [T, E], bias fp32 [E] -> (ids int32 [T, k], affinity fp32 [T, k])."""
     T, E = logits.shape
     if ids is None:
-        ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+        ids = _new((T, k), torch.int32, logits.device, stream)
     if affinity is None:
-        affinity = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+        affinity = _new((T, k), torch.float32, logits.device, stream)
     fg8_route_topk(logits, bias, T, E, k, ids, affinity, stream)
     return ids, affinity
