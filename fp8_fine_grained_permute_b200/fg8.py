@@ -374,7 +374,11 @@ def _bf16(x):
     return x
 
 
-_device = getattr(torch._C, "_cuda_getDevice", None)   # the current device's number, without a lazy check
+def _no_cuda():
+    raise RuntimeError("this torch has no CUDA")
+
+
+_device = getattr(torch._C, "_cuda_getDevice", _no_cuda)   # the current device's number, without a lazy check
 
 
 def _here():

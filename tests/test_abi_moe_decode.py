@@ -62,3 +62,24 @@ def test_helper_refuses(L):
         fg8.moe_decode(x, *w, 1, ids=z(3, 1, dt=torch.int32), affinity=z(3, 1, dt=f32), workspace=z(1))
     with pytest.raises(ValueError, match="64 tokens"):
         fg8.moe_decode_workspace(65, 1, 128, 128)
+
+
+def test_helper_refuses_in_a_torch_without_cuda(L, monkeypatch):
+    """Such a torch lacks the private functions that look the device and stream up."""
+    import importlib.util
+    for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+        monkeypatch.delattr(torch._C, name, raising=False)
+    spec = importlib.util.spec_from_file_location("fp8_fine_grained_permute_b200.fg8_without_cuda", fg8.__file__)
+    bare = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(bare)
+    z = lambda *s, dt=torch.uint8: torch.zeros(s, dtype=dt)   # noqa: E731
+    f32, i32 = torch.float32, torch.int32
+    with pytest.raises(ValueError, match="CUDA"):
+        bare.moe_decode(z(3, 128, dt=torch.bfloat16), z(2, 256, 128), z(2, 2, 1, dt=f32), z(2, 128, 128),
+                        z(2, 1, 1, dt=f32), 1, ids=z(3, 1, dt=i32), affinity=z(3, 1, dt=f32), workspace=z(1))
+    with pytest.raises(ValueError, match="CUDA"):
+        bare.requantize_colwise(z(128, 128), z(1, 128, dt=f32), z(2, dt=i32))
+    with pytest.raises(ValueError, match="CUDA"):
+        bare.gate_weights(z(6, dt=i32), z(3, 2, dt=f32), 6)
+    with pytest.raises(ValueError, match="CUDA"):
+        bare.route_topk(z(3, 4, dt=f32), z(4, dt=f32), 2)
