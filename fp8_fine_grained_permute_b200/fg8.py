@@ -163,7 +163,8 @@ def _ptr(t):
 
 def _stream(stream) -> int:
     if stream is None:   # the current stream's handle, without building a Stream object
-        return torch._C._cuda_getCurrentRawStream(_device())
+        device = _device()   # first: it raises where torch lacks the next line's function
+        return torch._C._cuda_getCurrentRawStream(device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
