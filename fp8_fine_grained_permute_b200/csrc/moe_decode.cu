@@ -132,7 +132,7 @@ struct Cfg {
     static constexpr uint32_t kOffRed = kOffFactors + kSlots * 2 * N * 4;   // float [2][4][N]
     static constexpr uint32_t kOffBars = kOffRed + 2 * 4 * N * 4;
     static constexpr int kNumBars = 2 * kStages + 2 * kTmemBufs + 4;    // full, empty, tfull, tempty, drain, group, x, h
-    static constexpr uint32_t kOffMisc = kOffBars + 8 * kNumBars;           // tmem slot, abort, call number
+    static constexpr uint32_t kOffMisc = kOffBars + 8 * kNumBars;           // tmem slot, abort, call number, -, filled[4]
     static constexpr uint32_t kOffPlan = kOffMisc + 32;
     static constexpr uint32_t kOffGroups = kOffPlan + 128;        // uint32 [kPairs]: n | first << 6 | expert << 16
     static constexpr uint32_t kOffList = kOffGroups + 4 * kPairs;   // uint32 [kPairs]: pair | token << 16, experts ascending
@@ -145,6 +145,7 @@ struct Cfg {
     static_assert(kSmem <= 232448, "shared memory per CTA");
     static_assert(kStage % 1024 == 0, "swizzle atoms");
     static_assert(sizeof(Plan) <= 128, "plan");
+    static_assert(kFillWarps == 4, "filled[4], step mod 4");
 };
 
 // workspace: a head of counters and the partials of cut units, both at fixed places
@@ -209,6 +210,22 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile i
 }
 FG8_DEV bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag, int32_t* status) {
     return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort_flag, status);
+}
+
+// After an abort, with every role done: no copy may reach this CTA's shared memory
+// once the CTA is gone.  The last `stages` issued steps lie each on its own stage,
+// the phases before them are complete; where the fill warp of a step (step mod 4)
+// gave up before it, its arrival is made up for, so that a stage's phase completes
+// with the bytes.  Bounded, as everything.
+__device__ __noinline__ void land_copies(uint32_t bar0, int stages, int issued, const int32_t* filled) {
+#pragma unroll 1
+    for (int m = max(0, issued - stages); m < issued; ++m) {
+        const uint32_t bar = bar0 + 8u * (m % stages), parity = (uint32_t)(m / stages) & 1u;
+        if (m >= filled[m & 3]) mbar_arrive(bar);
+        const uint64_t t0 = fg8::globaltimer_ns();
+        while (!mbar_try_wait(bar, parity) && fg8::globaltimer_ns() - t0 < 100000000ull) {
+        }
+    }
 }
 
 FG8_DEV void red_release_gpu(uint32_t* p, uint32_t v) {
@@ -376,6 +393,7 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + K::kOffMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + K::kOffMisc + 4);
     volatile uint32_t* s_call = reinterpret_cast<volatile uint32_t*>(smem + K::kOffMisc + 8);
+    int32_t* s_filled = reinterpret_cast<int32_t*>(smem + K::kOffMisc + 16);   // a fill warp's first step not filled
     uint32_t* s_groups = reinterpret_cast<uint32_t*>(smem + K::kOffGroups);
     uint32_t* s_list = reinterpret_cast<uint32_t*>(smem + K::kOffList);
     float* s_w = reinterpret_cast<float*>(smem + K::kOffW);
@@ -558,12 +576,14 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
     auto group_e = [&](uint32_t g) { return (int)(g >> 16); };
 
     bool ok = true;
+    int issued = 0;   // steps whose copies the producer has started
     if (warp == 0) {
         if (lane == 0) {
             // -------------------------------------------- weight producer
             uint32_t stage = 0, phase = 0;
             auto take = [&]() { return wait_bar(empty_bar(stage), phase ^ 1u, abort_flag, a.status); };
             auto next = [&]() {
+                ++issued;
                 if (++stage == S) {
                     stage = 0;
                     phase ^= 1u;
@@ -602,12 +622,6 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
                         k2 = 0;
                         if (++g == G) g = 0, ++cb;
                     }
-                }
-            }
-            if (!ok) {   // let copies already issued land before the CTA winds down
-                const uint32_t last = (stage + S - 1) % S, lp = stage == 0 ? (phase ^ 1u) : phase;
-                const uint64_t t0 = fg8::globaltimer_ns();
-                while (!mbar_try_wait(full_bar(last), lp) && fg8::globaltimer_ns() - t0 < 100000000ull) {
                 }
             }
         }
@@ -795,6 +809,7 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
                 next();
             }
         }
+        if (lane == 0) s_filled[fw] = n;
     } else if (warp >= 4) {
         // ------------------------------------------------ promotion
         const int quarter = warp & 3;
@@ -1029,6 +1044,7 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
 
     tc_fence_before();
     __syncthreads();
+    if (tid == 0 && *abort_flag) land_copies(bar0, S, issued, s_filled);
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(K::kTmemCols)

@@ -410,3 +410,39 @@ def test_input_codes_are_the_quantizers_bit_for_bit():
     got_s = ws[at:at + 4 * T * (C // 128)].view(torch.float32).view(T, C // 128)
     assert torch.equal(got_s.t(), want_s)
     assert torch.equal(got_q, want_q)
+
+
+def _winds_down(L, x, k, routing, head, status, limit, T):
+    """A call whose counters are set to `head` (int32 words of the workspace's first
+    4096 bytes) gives up with `status`; the context stays usable, and with the
+    workspace zeroed again the next call is right."""
+    import time
+    ws = fg8.moe_decode_workspace(T, k, L.C, L.I)
+    want = run(L, x, k, logits=routing[0], bias=routing[1])[0]
+    words = ws[:4096].view(torch.int32)
+    words[:len(head)] = torch.tensor(head, dtype=torch.int32, device="cuda")
+    before = words.clone()
+    st = fg8.new_status()
+    torch.cuda.synchronize()
+    t0 = time.monotonic()
+    fg8.moe_decode(x, *L.weights(), k, logits=routing[0], bias=routing[1], workspace=ws, dev_status=st)
+    torch.cuda.synchronize()
+    assert time.monotonic() - t0 < limit
+    assert st.item() == status
+    after = words.clone()
+    ws.zero_()
+    for _ in range(2):
+        assert torch.equal(run(L, x, k, ws=ws, logits=routing[0], bias=routing[1])[0], want)
+    return before, after
+
+
+@pytest.mark.parametrize("T,E,k,C,I", [(1, 64, 6, 2048, 768), (20, 8, 4, 512, 256), (2, 3, 2, 256, 128)])
+def test_codes_that_never_come_time_out(T, E, k, C, I):
+    """The counter of CTAs that have written x's codes starts so far behind that the
+    wait runs out, with weight copies in flight and few or many steps a CTA: the call
+    reports it, lands its copies and ends; no CTA goes on to the next meeting."""
+    L = Layer(E, C, I, seed=84)
+    before, after = _winds_down(L, L.x(T), k, L.routing(T), [-10_000_000], fg8.FG8_ERR_TIMEOUT, 30.0, T)
+    ctas = torch.cuda.get_device_properties(0).multi_processor_count
+    assert after[0].item() == before[0].item() + ctas      # every CTA wrote its codes
+    assert (after[2:2 + ctas] == 0).any()                  # CTAs with a share of the up-projection did not finish
