@@ -112,6 +112,14 @@ FG8_DEV uint32_t code_pair(float x, float y, float inv) {
     if (kExact && inv < 0.f) return fg8::cvt_e4m3x2(__fdiv_rn(x, -inv), __fdiv_rn(y, -inv));
     return fg8::cvt_e4m3x2(x * inv, y * inv);
 }
+// Let copies already issued land before the CTA winds down: those of item n, whose
+// wait ran out, and of the one after it, if the CTA has one (bounded).
+__device__ __noinline__ void land_copies(uint32_t bars, int n, int items) {
+    auto landed = [&](int m) { return m >= items || mbar_try_wait(bars + 8u * (m & 1), (m >> 1) & 1); };
+    const uint64_t t0 = fg8::globaltimer_ns();
+    while (!(landed(n) && landed(n + 1)) && fg8::globaltimer_ns() - t0 < 100000000ull) {
+    }
+}
 FG8_DEV float2 splat(float x) { return make_float2(x, x); }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -183,7 +191,6 @@ act_backward(const __grid_constant__ CUtensorMap tm_dh, const __grid_constant__ 
     factors_landed();
     __syncthreads();
 
-    bool ok = true;
     for (int it = i0; it < i1; ++it) {
         const int n = it - i0, st = n & 1;
         if (it + 1 < i1) {
@@ -194,7 +201,7 @@ act_backward(const __grid_constant__ CUtensorMap tm_dh, const __grid_constant__ 
         const uint8_t* sdh = smem + st * kStage + 8 * lane;
         const uint32_t a_g = sbase + st * kStage + kDhBytes + 4 * lane;   // gate codes; up codes kCodeBytes further on
         const int r0 = kRows * warp;
-        ok = mbar_wait(full_bar(st), (n >> 1) & 1, abort_flag, a.status);
+        const bool ok = mbar_wait(full_bar(st), (n >> 1) & 1, abort_flag, a.status);
 
         // rows that no expert owns may hold anything: zeros in their place (the rows
         // of a tile that belong to the next expert are finite; their factors are 0)
@@ -307,8 +314,9 @@ act_backward(const __grid_constant__ CUtensorMap tm_dh, const __grid_constant__ 
         }
         // all warps' maxima are there
         if (!__syncthreads_and(ok)) {
-            ok = false;
-            break;
+            factors_landed();
+            if (tid == 0) land_copies(full_bar(0), n, i1 - i0);
+            return;
         }
         // ---- column scales
         if (tid < 384) {
@@ -434,12 +442,6 @@ act_backward(const __grid_constant__ CUtensorMap tm_dh, const __grid_constant__ 
         if (++cb == ncb) {
             cb = 0;
             if (it + 1 < i1) cur = tile_of(cur.tile + 1);
-        }
-    }
-    if (!ok && tid == 0) {   // let copies already issued land before the CTA winds down
-        const uint64_t t0 = fg8::globaltimer_ns();
-        while (!(mbar_try_wait(full_bar(0), 0) && mbar_try_wait(full_bar(1), 0)) &&
-               fg8::globaltimer_ns() - t0 < 100000000ull) {
         }
     }
 }
