@@ -56,7 +56,8 @@
 // against 18.0 us at 64.
 //
 // Every wait is bounded (FG8_ERR_TIMEOUT in *status; the roles wind down and TMEM
-// is released).
+// is released).  A meeting with more arrivals than CTAs is one with another call on
+// the same workspace: the call ends there in the same way (FG8_ERR_WORKSPACE_SHARED).
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -698,7 +699,10 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
                         *abort_flag = 1;
                     }
                 }
-                if (over > 0) fg8::set_status(a.status, FG8_ERR_WORKSPACE_SHARED);   // another call arrives here too
+                if (over > 0) {   // another call arrives here too: what was waited for may not be there
+                    fg8::set_status(a.status, FG8_ERR_WORKSPACE_SHARED);
+                    *abort_flag = 1;
+                }
                 mbar_arrive(bar);
             }
             __syncwarp();

@@ -749,7 +749,8 @@ def grouped_gemm_combine(a, sa, b, sb, offsets, row_token, token_row, affinity, 
 
 def moe_decode_workspace(T, k, C, I, device=None, stream=None):
     """A zeroed workspace for moe_decode calls of up to T tokens (kept by the
-    caller: a call leaves it ready for the next).  It is zeroed on `stream` (default:
+    caller: a call leaves it ready for the next; zero it again after one that reported
+    FG8_ERR_TIMEOUT or FG8_ERR_WORKSPACE_SHARED).  It is zeroed on `stream` (default:
     the current one)."""
     n = fg8_moe_decode_workspace(T, k, C, I)
     if n == 0:
@@ -765,7 +766,9 @@ def moe_decode(x, wq_up, sw_up, wq_dn, sw_dn, k, logits=None, bias=None, ids=Non
     [T, E] and bias [E] (routing included; ids and affinity are then outputs) or
     ids int32 [T, k] and affinity fp32 [T, k] -> (out [T, C], ids, affinity).
     workspace: moe_decode_workspace(...), kept from call to call (without one each
-    call zeroes its own); calls that overlap on the GPU need their own."""
+    call zeroes its own); calls that overlap on the GPU need their own.  A call that
+    reports FG8_ERR_WORKSPACE_SHARED or FG8_ERR_TIMEOUT in dev_status stopped early: `out`
+    is unspecified and the workspace is to be zeroed before the next."""
     T, C = x.shape
     E, I, dev = wq_up.shape[0], wq_dn.shape[2], x.device
     f32, u8, i32 = torch.float32, torch.uint8, torch.int32

@@ -518,10 +518,12 @@ fg8_status fg8_grouped_gemm_combine(const uint8_t* a, const float* sa, const uin
  *   workspace  >= fg8_moe_decode_workspace(T, k, C, I) bytes, 16-byte aligned,
  *              zeroed once, before the first call (its first
  *              FG8_MOE_DECODE_HEAD bytes hold counters and tagged partial sums).
- *              A call leaves it ready for the next one of any size; after one that
- *              reported FG8_ERR_TIMEOUT it is to be zeroed again.
- *              Calls that overlap on the GPU need their own workspace
- *              (FG8_ERR_WORKSPACE_SHARED where that is noticed).
+ *              A call leaves it ready for the next one of any size.
+ *              Calls that overlap on the GPU need their own workspace: where that is
+ *              noticed, the call stops with FG8_ERR_WORKSPACE_SHARED.
+ *              After a call that reported FG8_ERR_WORKSPACE_SHARED or FG8_ERR_TIMEOUT
+ *              `out` is unspecified, and the workspace is to be zeroed again (its
+ *              counters are out of step: every later call would report it too).
  *   T <= 64, 1 <= k <= min(16, E), E <= 1024, C % 128 == 0, I % 128 == 0;
  *   x, wq_up, wq_dn, out 16-byte aligned.  NaN logits are outside the contract.
  *   A cooperative launch (one CTA per SM); every wait is bounded

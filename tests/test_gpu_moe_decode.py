@@ -446,3 +446,27 @@ def test_codes_that_never_come_time_out(T, E, k, C, I):
     ctas = torch.cuda.get_device_properties(0).multi_processor_count
     assert after[0].item() == before[0].item() + ctas      # every CTA wrote its codes
     assert (after[2:2 + ctas] == 0).any()                  # CTAs with a share of the up-projection did not finish
+
+
+@pytest.mark.parametrize("T,E,k,C,I", [(1, 64, 6, 2048, 768), (20, 8, 4, 512, 256), (2, 3, 2, 256, 128)])
+@pytest.mark.parametrize("meeting", [0, 1])
+def test_a_workspace_that_another_call_uses_stops_the_call(T, E, k, C, I, meeting):
+    """A meeting's counter holds the arrivals of another call's CTAs, as two calls at
+    once on one workspace leave it: the call reports it and ends without going on to
+    what it could not wait for, and says so again until the workspace is zeroed."""
+    L = Layer(E, C, I, seed=85)
+    x, routing = L.x(T), L.routing(T)
+    ctas = torch.cuda.get_device_properties(0).multi_processor_count
+    head = [2 * ctas] if meeting == 0 else [0, 2 * ctas]
+    before, after = _winds_down(L, x, k, routing, head, fg8.FG8_ERR_WORKSPACE_SHARED, 10.0, T)
+    assert after[0].item() == before[0].item() + ctas
+    if meeting == 0:
+        assert (after[2:2 + ctas] == 0).any()    # CTAs with a share of the up-projection did not finish
+    # a workspace with both counters ahead, as after such a call
+    ws = fg8.moe_decode_workspace(T, k, C, I)
+    ws[:4096].view(torch.int32)[:2] = ctas
+    for _ in range(2):
+        st = fg8.new_status()
+        fg8.moe_decode(x, *L.weights(), k, logits=routing[0], bias=routing[1], workspace=ws, dev_status=st)
+        torch.cuda.synchronize()
+        assert st.item() == fg8.FG8_ERR_WORKSPACE_SHARED
