@@ -213,6 +213,11 @@ FG8_DEV bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag, i
     return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort_flag, status);
 }
 
+__device__ __noinline__ void stop_call(int32_t code, volatile int* abort_flag, int32_t* status) {
+    fg8::set_status(status, code);
+    *abort_flag = 1;
+}
+
 // After an abort, with every role done: no copy may reach this CTA's shared memory
 // once the CTA is gone.  The last `stages` issued steps lie each on its own stage,
 // the phases before them are complete; where the fill warp of a step (step mod 4)
@@ -258,10 +263,7 @@ FG8_DEV float value_of(uint64_t w) { return __uint_as_float((uint32_t)w); }
 __device__ __noinline__ bool try_again(uint64_t& t0, volatile int* abort_flag, int32_t* status) {
     const uint64_t now = fg8::globaltimer_ns();
     if (t0 == 0) t0 = now;
-    if (now - t0 > fg8::kWaitLimitNs) {
-        fg8::set_status(status, FG8_ERR_TIMEOUT);
-        *abort_flag = 1;
-    }
+    if (now - t0 > fg8::kWaitLimitNs) stop_call(FG8_ERR_TIMEOUT, abort_flag, status);
     return !*abort_flag;
 }
 
@@ -694,15 +696,10 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
                 const uint64_t t0 = fg8::globaltimer_ns();
                 int32_t over;
                 while ((over = (int32_t)(fg8::ld_acquire_gpu(arrivals) - all)) < 0 && !*abort_flag) {
-                    if (fg8::globaltimer_ns() - t0 > fg8::kWaitLimitNs) {
-                        fg8::set_status(a.status, FG8_ERR_TIMEOUT);
-                        *abort_flag = 1;
-                    }
+                    if (fg8::globaltimer_ns() - t0 > fg8::kWaitLimitNs) stop_call(FG8_ERR_TIMEOUT, abort_flag, a.status);
                 }
-                if (over > 0) {   // another call arrives here too: what was waited for may not be there
-                    fg8::set_status(a.status, FG8_ERR_WORKSPACE_SHARED);
-                    *abort_flag = 1;
-                }
+                // another call arrives here too: what was waited for may not be there
+                if (over > 0) stop_call(FG8_ERR_WORKSPACE_SHARED, abort_flag, a.status);
                 mbar_arrive(bar);
             }
             __syncwarp();
