@@ -643,11 +643,12 @@ def grouped_gemm_swiglu_quant_save(a, sa, b, sb, offsets, hq=None, sh=None, guq=
 
 def swiglu_backward_quant(dh, guq, sgu, offsets, row_w=None, dq=None, sd=None, dqT=None, sdT=None,
                           hqT=None, shT=None, gate_dot=None, offsets_out=None, dev_status=None,
-                          stream=None):
+                          stream=None, want_dots=True):
     """dh bf16 [R, I] (gradient of the activation's output), guq/sgu (the 8-bit
     gate and up) -> dict of the [dG dU] operand by rows (dq, sd) and by columns
     (dqT, sdT), the weighted activation by columns (hqT, shT), gate_dot
-    [I/128, R] and the padded offsets_out."""
+    [I/128, R] and the padded offsets_out.  want_dots=False (the gates are not
+    trained): no gate_dot."""
     R, I = dh.shape
     E, dev = offsets.numel() - 1, dh.device
     P = fg8_colwise_capacity(R, E)
@@ -658,7 +659,7 @@ def swiglu_backward_quant(dh, guq, sgu, offsets, row_w=None, dq=None, sd=None, d
     sdT = _new((P // 128, 2 * I), f32, dev, stream) if sdT is None else sdT
     hqT = _new((I, P), u8, dev, stream) if hqT is None else hqT
     shT = _new((P // 128, I), f32, dev, stream) if shT is None else shT
-    gate_dot = _new((I // 128, R), f32, dev, stream) if gate_dot is None else gate_dot
+    gate_dot = _new((I // 128, R), f32, dev, stream) if gate_dot is None and want_dots else gate_dot
     offsets_out = _new((E + 1,), i32, dev, stream) if offsets_out is None else offsets_out
     here = _here()
     _call("fg8_swiglu_backward_quant", stream,
@@ -668,7 +669,7 @@ def swiglu_backward_quant(dh, guq, sgu, offsets, row_w=None, dq=None, sd=None, d
         _arg("dq", dq, (R, 2 * I), u8, here), _arg("sd", sd, (2 * I // 128, R), f32, here),
         _arg("dqT", dqT, (2 * I, P), u8, here), _arg("sdT", sdT, (P // 128, 2 * I), f32, here),
         _arg("hqT", hqT, (I, P), u8, here), _arg("shT", shT, (P // 128, I), f32, here),
-        _arg("gate_dot", gate_dot, (I // 128, R), f32, here),
+        None if gate_dot is None else _arg("gate_dot", gate_dot, (I // 128, R), f32, here),
         _arg("offsets_out", offsets_out, (E + 1,), i32, here), _raw(dev_status, here))
     return dict(dq=dq, sd=sd, dqT=dqT, sdT=sdT, hqT=hqT, shT=shT, gate_dot=gate_dot,
                 offsets_out=offsets_out)
@@ -710,21 +711,25 @@ def gate_weights(token_row, affinity, R, normalize=True, row_w=None, stream=None
 
 
 def gate_backward(gate_dot, token_row, topk_ids, affinity, E, normalize=True, daffinity=None,
-                  dlogits=None, stream=None):
+                  dlogits=None, stream=None, want_dlogits=True):
     """gate_dot fp32 [I/128, R] (swiglu_backward_quant) -> (daffinity [T, k],
-    dlogits [T, E]): the gradients of the chosen affinities and router logits."""
+    dlogits [T, E]): the gradients of the chosen affinities and router logits.
+    want_dlogits=False: (daffinity, None), and topk_ids may be None."""
     nb, R = gate_dot.shape
     T, k = affinity.shape
     f32, i32, dev = torch.float32, torch.int32, affinity.device
     daffinity = _new((T, k), f32, dev, stream) if daffinity is None else daffinity
-    dlogits = _new((T, E), f32, dev, stream) if dlogits is None else dlogits
+    dlogits = _new((T, E), f32, dev, stream) if dlogits is None and want_dlogits else dlogits
+    if dlogits is not None and topk_ids is None:
+        raise ValueError("gate_backward needs topk_ids for dlogits")
     here = _here()
     _call("fg8_gate_backward", stream, _arg("gate_dot", gate_dot, (nb, R), f32, here), nb, R,
                                    _arg_n("token_row", token_row, T * k, i32, here),
-                                   _arg_n("topk_ids", topk_ids, T * k, i32, here),
+                                   None if topk_ids is None and dlogits is None
+                                   else _arg_n("topk_ids", topk_ids, T * k, i32, here),
                                    _arg("affinity", affinity, (T, k), f32, here), T, k, E,
                                    int(bool(normalize)), _arg("daffinity", daffinity, (T, k), f32, here),
-                                   _arg("dlogits", dlogits, (T, E), f32, here))
+                                   None if dlogits is None else _arg("dlogits", dlogits, (T, E), f32, here))
     return daffinity, dlogits
 
 

@@ -128,3 +128,18 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
         with pytest.raises(ValueError, match="cuda:0, current device cuda:1"):
             take(_Elsewhere(0))
     assert fg8._raw(None) is None
+
+
+def test_left_out_dots_and_logits(L):
+    """What may be left out is refused with the rest of the arguments, not for its absence."""
+    z = lambda *s, dt=torch.uint8: torch.zeros(s, dtype=dt)   # noqa: E731
+    f32, i32 = torch.float32, torch.int32
+    with pytest.raises(ValueError, match="topk_ids"):
+        fg8.gate_backward(z(1, 6, dt=f32), z(6, dt=i32), None, z(3, 2, dt=f32), 4)
+    with pytest.raises(ValueError, match="CUDA"):
+        fg8.gate_backward(z(1, 6, dt=f32), z(6, dt=i32), None, z(3, 2, dt=f32), 4, want_dlogits=False)
+    with pytest.raises(ValueError, match="CUDA"):
+        fg8.swiglu_backward_quant(z(6, 128, dt=torch.bfloat16), z(6, 256), z(2, 6, dt=f32), z(2, dt=i32), want_dots=False)
+    with pytest.raises(ValueError, match="gate_dot"):
+        fg8.swiglu_backward_quant(z(6, 128, dt=torch.bfloat16), z(6, 256), z(2, 6, dt=f32), z(2, dt=i32),
+                                  gate_dot=z(2, 6, dt=f32), want_dots=False)

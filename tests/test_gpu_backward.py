@@ -631,3 +631,39 @@ def test_act_backward_gates_beyond_the_integers_of_fp32(oracle):
     du = (d * u)[:6]
     big = np.abs(du) > 0.1 * np.abs(du).max(1, keepdims=True)
     assert np.all((np.abs(got - du) <= 2.0 ** -4 * 1.01 * np.abs(du))[big])
+
+
+# ---------------------------------------------------------------------------
+# without the router's gradient
+# ---------------------------------------------------------------------------
+
+def test_act_backward_without_dots_is_the_same():
+    counts = [130, 0, 61]
+    c = act_case(counts, 256, seed=41, extra_rows=3)
+    g = lambda x: torch.from_numpy(np.ascontiguousarray(x)).cuda()   # noqa: E731
+    args = c["dh"].cuda(), g(c["guq"]), g(c["sgu"]), g(offsets_of(counts))
+    n, used = sum(counts), int(padded(counts)[-1])
+    st = fg8.new_status()
+    want = fg8.swiglu_backward_quant(*args, row_w=g(c["w"]), dev_status=st)
+    got = fg8.swiglu_backward_quant(*args, row_w=g(c["w"]), want_dots=False, dev_status=st)
+    torch.cuda.synchronize()
+    assert st.item() == 0 and got["gate_dot"] is None and want["gate_dot"] is not None
+    for k, cut in (("dq", lambda t: t[:n]), ("sd", lambda t: t[:, :n]), ("dqT", lambda t: t[:, :used]),
+                   ("sdT", lambda t: t[:used // 128]), ("hqT", lambda t: t[:, :used]),
+                   ("shT", lambda t: t[:used // 128]), ("offsets_out", lambda t: t)):
+        assert torch.equal(cut(got[k]), cut(want[k])), k
+
+
+@pytest.mark.parametrize("normalize", [True, False])
+def test_gate_backward_without_logits_is_the_same(normalize):
+    T, E, k, nb = 77, 9, 3, 5
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    aff = torch.rand(T, k, device="cuda", generator=gen)
+    ids = torch.randint(0, E, (T, k), device="cuda", generator=gen, dtype=torch.int32)
+    tr = torch.randperm(T * k, device="cuda", generator=gen).to(torch.int32)
+    tr[7] = -1
+    dot = torch.randn(nb, T * k, device="cuda", generator=gen)
+    want, dlogits = fg8.gate_backward(dot, tr, ids, aff, E, normalize=normalize)
+    got, none = fg8.gate_backward(dot, tr, None, aff, E, normalize=normalize, want_dlogits=False)
+    torch.cuda.synchronize()
+    assert none is None and dlogits is not None and torch.equal(got, want)
