@@ -894,7 +894,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                     break;
                 }
                 amax = fmaxf(amax, s_amax[(grp ^ 1) * BM + r]);
-                const float sc = fg8::tile_scale(amax);
+                const float sc = fg8::tile_scale32(amax);
                 const int I = a.N / 2;
                 uint8_t* const h0 = static_cast<uint8_t*>(a.out) + col0 + 64 * grp;
                 if (kSave) {

@@ -19,8 +19,9 @@
  *     q = E4M3(fp32(x / s))  round to nearest, ties to even, saturating at
  *                            +-448, sign of zero kept.
  * s is the dequantization multiplier: x ~= q * s.  (The calls that quantize fp32
- * values down the token axis or save them take s = 2^-149 where amax / 448 rounds
- * to 0.)  NaN/Inf inputs are outside
+ * values -- h and the checkpoint of the gated up-projections, the activation's
+ * backward, rows kept in 8 bits, h in fg8_moe_decode -- take s = 2^-149 where
+ * amax / 448 rounds to 0, which no tile of bf16 values reaches.)  NaN/Inf inputs are outside
  * the contract (their outputs are unspecified).
  *
  * Conventions for every call:

@@ -408,7 +408,8 @@ void fg8o_gemm_mgrouped_entries(const uint8_t* a, const float* sa, int64_t M_tot
  *     h = silu(g) * u,   silu(g) = g / (1 + exp(-g)),
  * evaluated in fp64 from the fp64 up-projection (g: gate half, u: up half),
  * then rounded once to fp32 and quantized as 1x128 tiles exactly as above
- * (amax of the fp32 values, s = fp32_RN(amax / 448), q = E4M3(fp32_RN(h / s))).
+ * (amax of the fp32 values, s = fp32_RN(amax / 448), 2^-149 where that rounds to 0,
+ * q = E4M3(fp32_RN(h / s))).
  *   G, U  fp64 [R][I] (row-major), I % 128 == 0
  *   h     fp64 [R][I] out: the activation before rounding (may be NULL)
  *   hq    E4M3 [R][I];  sh fp32 [I/128][R]: sh[c*R + r] scales row r, block c */
@@ -430,6 +431,8 @@ void fg8o_swiglu_quantize(const double* G, const double* U, int64_t R, int64_t I
                     amax = fabsf(hf[i]);
             }
             float s = fg8o_tile_scale(amax);
+            if (s == 0.0f)
+                s = 0x1p-149f;      /* fp32 values can be that small; no code is x / 0 */
             for (int i = 0; i < 128; ++i)
                 hq[r * I + c * 128 + i] = quant_elem(hf[i], s);
             sh[c * R + r] = s;

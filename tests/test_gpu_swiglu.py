@@ -226,3 +226,33 @@ def test_swiglu_quant_rejects_bad_shapes():
     with pytest.raises(fg8.FG8Error) as ei:
         fg8.fg8_grouped_gemm_swiglu_quant(a, sa, b, sb, off, 128, 96, 256, 1, hq, sh, None)
     assert ei.value.status == fg8.FG8_ERR_INVALID_ARG
+
+
+def test_h_whose_scale_rounds_to_zero(oracle):
+    """Tiles whose largest |h| is below 448 * 2^-150: amax / 448 rounds to 0, the scale
+    is 2^-149, and the codes are h / 2^-149 (a whole number: h is a multiple of it),
+    not quotients by 0.  Both forms of the gated up-projection."""
+    K, I, n = 128, 128, 40
+    a = torch.zeros((n, K), dtype=torch.uint8, device="cuda")
+    a[:, 0] = 0x38                                       # x = (1, 0, ..)
+    sa = torch.ones((1, n), device="cuda")
+    sa[0, 5:] = 2.0                                      # gates of 4
+    b = torch.zeros((1, 2 * I, K), dtype=torch.uint8, device="cuda")
+    b[0, :I, 0] = 0x40                                   # gate weight 2: silu(2) = 1.7616, silu(4) = 3.928
+    up = torch.zeros(I)
+    up[1:] = 2.0 ** (torch.arange(1, I) % 5).float()     # ups 0, 1 .. 16 times 2^-148
+    b[0, I:, 0] = up.to(torch.float8_e4m3fn).view(torch.uint8).cuda()
+    sb = torch.tensor([[[1.0], [2.0 ** -148]]], device="cuda")
+    off = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    hq, sh = fg8.grouped_gemm_swiglu_quant(a, sa, b, sb, off)
+    hq2, sh2, guq, sgu = fg8.grouped_gemm_swiglu_quant_save(a, sa, b, sb, off)
+    torch.cuda.synchronize()
+    g = np.where(np.arange(n) < 5, 2.0, 4.0)[:, None]
+    u = up.numpy().astype(np.float64)[None] * 2.0 ** -148 * (g / 2)
+    m = g / (1 + np.exp(-g)) * u / 2.0 ** -149           # at most 3.93 * 16 * 4 = 252 units
+    # rows 0..4: amax / 448 below half a unit; the others: it rounds to one by itself
+    assert m[:5].max() < 448 / 2 < m.max() < 448 and np.all(sh.cpu().numpy() == np.float32(2.0 ** -149))
+    got = oracle.e4m3_decode_table()[hq.cpu().numpy()].astype(np.float64)
+    # the product rounds to a whole unit, the code to E4M3
+    assert np.all(np.abs(got - m) <= 0.5 + 2.0 ** -4 * (m + 0.5)) and np.all(got[:, 0] == 0)
+    assert torch.equal(hq, hq2) and torch.equal(sh, sh2)

@@ -83,3 +83,12 @@ def test_every_tile_maximum_maps_to_448(oracle, seed):
             deq = dq[hq[r, 128 * c:128 * (c + 1)]] * np.float64(sh[c, r])
             lim = np.maximum(2.0 ** -4 * np.abs(t), 2.0 ** -10 * np.float64(sh[c, r]))
             assert np.all(np.abs(deq - t) <= lim * (1 + 1e-12))
+
+
+def test_scale_that_rounds_to_zero(oracle):
+    """h below 448 * 2^-150: the scale is 2^-149 and the codes are h in its units."""
+    G = np.full((1, 128), 40.0)                      # silu(40) = 40
+    U = np.arange(128, dtype=np.float64)[None] % 5 * 2.0 ** -149 / 40
+    h, hq, sh = oracle.swiglu_quantize(G, U)
+    assert sh[0, 0] == np.float32(2.0 ** -149)
+    assert np.array_equal(oracle.e4m3_decode_table()[hq[0]], np.arange(128) % 5)
