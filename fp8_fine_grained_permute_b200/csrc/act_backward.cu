@@ -26,15 +26,16 @@
 //   * the column codes (8 tokens of a column a thread) are turned around through
 //     shared memory, 8-byte pieces XOR-swizzled by column, and leave as 128-byte
 //     lines of the token axis.
-// On a B200: 426 us for 65536 rows x 2048 in 256 experts (1.24 GB: 2.9 TB/s, 45 %
+// On a B200: 430 us for 65536 rows x 2048 in 256 experts (1.24 GB: 2.9 TB/s, 45 %
 // of the measured copy rate), 24 us for 1998 rows x 768 in 64.  The instructions
-// bound it: with every store taken out it still takes 383 us, with the special
-// functions out as well 374; 55 instructions an element at 57 % of the issue slots,
-// the conversion, maximum and byte-permute pipe busiest.  Measured and not kept: two
-// CTAs an SM, each with 64 of a tile's rows and the column maxima exchanged over a
-// cluster pair (490 us); the row maxima, reciprocals and doubled factors through
-// shared memory in place of shuffles and moves (fewer instructions, but 436 to
-// 487 us); stores put off into the next item (slower).
+// bound it: when it took 426 us, 383 were left with every store taken out and 374
+// with the special functions out as well; 55 instructions an element at 57 % of the
+// issue slots, the conversion, maximum and byte-permute pipe busiest.  Measured and
+// not kept (each against 426): two CTAs an SM, each with 64 of a tile's rows and the
+// column maxima exchanged over a cluster pair (490 us); the row maxima, reciprocals
+// and doubled factors through shared memory in place of shuffles and moves (fewer
+// instructions, but 436 to 487 us); stores put off into the next item (slower); the
+// last factor of dG as (1 + g) - g sig, which is 4 us faster and wrong from 2^24 on.
 #include <type_traits>
 
 #include "fg8_columns.cuh"
@@ -203,8 +204,9 @@ act_backward(const __grid_constant__ CUtensorMap tm_dh, const __grid_constant__ 
         const int r0 = kRows * warp;
         const bool ok = mbar_wait(full_bar(st), (n >> 1) & 1, abort_flag, a.status);
 
-        // rows that no expert owns may hold anything: zeros in their place (the rows
-        // of a tile that belong to the next expert are finite; their factors are 0)
+        // rows that no expert owns may hold anything: zeros in their place.  (Rows of a
+        // tile that belong to the next expert have factors of 0: what is finite there
+        // is 0, the maxima drop the NaN that is left of the rest, its codes are masked.)
         if (cur.n_in < 128 && cur.row0 + 128 > owned) {
             const int first = max(cur.n_in, owned - cur.row0);
             uint8_t* stage = smem + st * kStage;

@@ -10,28 +10,6 @@ namespace fg8 {
 
 constexpr int kColsMaxE = 1024;
 
-// Two E4M3 codes (bits 7..0 and 15..8) -> fp32, exact.
-FG8_DEV float2 e4m3x2_f32(uint32_t codes) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
-    return __half22float2(*reinterpret_cast<const __half2*>(&h));
-}
-
-// Four E4M3 codes -> two pairs of fp32 values, without taking the word apart.
-FG8_DEV void e4m3x4_f32(uint32_t codes, float2& lo, float2& hi) {
-    uint32_t a, b;
-    asm("{\n"
-        ".reg .b16 l, h;\n"
-        "mov.b32 {l, h}, %2;\n"
-        "cvt.rn.f16x2.e4m3x2 %0, l;\n"
-        "cvt.rn.f16x2.e4m3x2 %1, h;\n"
-        "}\n"
-        : "=r"(a), "=r"(b)
-        : "r"(codes));
-    lo = __half22float2(*reinterpret_cast<const __half2*>(&a));
-    hi = __half22float2(*reinterpret_cast<const __half2*>(&b));
-}
-
 // Two E4M3 codes in shared memory -> fp32.  A 16-bit load hands the conversion its
 // operand as it is; taking a word apart costs two instructions of the pipe (ALU,
 // with the conversions, maxima and byte permutes) that bounds these kernels.
