@@ -675,7 +675,11 @@ moe_decode(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CU
     } else if (warp >= 8) {
         // ------------------------------------------------ operand B
         // fill warp w takes the steps n = w, w + 4, ...: the first use of a stage
-        // that is not yet free is at most one phase ahead (4 <= stages)
+        // that is not yet free is at most one phase ahead (4 <= stages).  That is all
+        // a wait by parity can tell apart, and it holds because one thread issues all
+        // MMAs: stages are released in the order of the steps, so the release of n - 4's
+        // stage, which this warp has waited for, comes after that of every stage before
+        // (tests/test_moe_decode_ring.py)
         const int fw = warp - 8;
         const int sub = lane >> 3, ch = lane & 7;   // a row's 128 codes: 8 lanes
         uint32_t stage = fw, phase = 0;
