@@ -699,7 +699,11 @@ extern "C" fg8_status fg8_quantize_act(const uint16_t* x, int64_t T, int64_t K,
 
     if (layout == FG8_COLWISE) {
         if (E < 1 || E > kMaxE) return E > kMaxE ? FG8_ERR_UNSUPPORTED : FG8_ERR_INVALID_ARG;
-        if (!offsets_in || !xqT || !saT || !offsets_out) return FG8_ERR_INVALID_ARG;
+        if (!offsets_in || !offsets_out) return FG8_ERR_INVALID_ARG;
+        if (T == 0)   // no rows (their buffers may be NULL), no columns
+            return cudaMemsetAsync(offsets_out, 0, sizeof(int32_t) * ((size_t)E + 1), st) == cudaSuccess
+                       ? FG8_OK : FG8_ERR_CUDA;
+        if (!xqT || !saT) return FG8_ERR_INVALID_ARG;
         if (row_token == nullptr && k != 1) return FG8_ERR_INVALID_ARG;
         if (!fg8h::aligned16(xqT) || !fg8h::aligned16(saT)) return FG8_ERR_INVALID_ARG;
         if (K / 128 > 65535) return FG8_ERR_UNSUPPORTED;

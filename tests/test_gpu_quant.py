@@ -485,3 +485,17 @@ def test_quantize_weight_all_ties_and_subnormal_scales(oracle, transposed):
         torch.cuda.synchronize()
     assert np.array_equal(wq.cpu().numpy(), rwq)
     assert np.array_equal(sw.cpu().numpy().view(np.uint32), rsw.view(np.uint32))
+
+
+@pytest.mark.parametrize("k", [1, 3])
+def test_colwise_of_no_rows(k):
+    """An empty batch: padded offsets of 0, whatever the buffers of its rows."""
+    x = torch.empty((0, 256), dtype=torch.bfloat16, device="cuda")
+    off = torch.zeros(5, dtype=torch.int32, device="cuda")
+    rows = torch.empty(0, dtype=torch.int32, device="cuda")
+    xqT, saT, pad = fg8.quantize_act_colwise(x, off, k=k, row_token=None if k == 1 else rows)
+    pad.fill_(9)
+    fg8.fg8_quantize_act(x.view(torch.int16), 0, 256, None, k, 4, off, fg8.FG8_COLWISE, None, None,
+                         None if k == 1 else rows, None, pad, xqT, saT, None, 0, None)
+    torch.cuda.synchronize()
+    assert xqT.shape[0] == 256 and not pad.any()
