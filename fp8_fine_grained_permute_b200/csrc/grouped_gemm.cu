@@ -1128,7 +1128,8 @@ extern "C" fg8_status fg8_grouped_gemm(const uint8_t* a, const float* sa, const 
                                        int N, int K, int E, int group_mode, int bscale_mode,
                                        int out_dtype, void* out, void* workspace, size_t ws_bytes,
                                        int32_t* dev_status, fg8_stream_t stream) {
-    if (!a || !sa || !b || !sb || !offsets || !out) return FG8_ERR_INVALID_ARG;
+    // (buffers of no rows may be NULL)
+    if ((M_total != 0 && (!a || !sa || !out)) || !b || !sb || !offsets) return FG8_ERR_INVALID_ARG;
     if (E < 1 || N < 128 || K < 128 || N % 128 || K % 128 || M_total < 0)
         return FG8_ERR_INVALID_ARG;
     if (E > kMaxE) return FG8_ERR_UNSUPPORTED;
@@ -1219,7 +1220,7 @@ static fg8_status launch_swiglu(const uint8_t* a, const float* sa, const uint8_t
                                 const int32_t* offsets, int64_t M_total, int I, int K, int E,
                                 uint8_t* hq, float* sh, uint8_t* guq, float* sgu, int32_t* dev_status,
                                 fg8_stream_t stream) {
-    if (!a || !sa || !b || !sb || !offsets || !hq || !sh) return FG8_ERR_INVALID_ARG;
+    if ((M_total != 0 && (!a || !sa || !hq || !sh)) || !b || !sb || !offsets) return FG8_ERR_INVALID_ARG;
     if (E < 1 || I < 128 || K < 128 || I % 128 || K % 128 || M_total < 0)
         return FG8_ERR_INVALID_ARG;
     if (E > kMaxE) return FG8_ERR_UNSUPPORTED;
@@ -1286,7 +1287,7 @@ extern "C" fg8_status fg8_grouped_gemm_swiglu_quant_save(const uint8_t* a, const
                                                          int K, int E, uint8_t* hq, float* sh,
                                                          uint8_t* guq, float* sgu, int32_t* dev_status,
                                                          fg8_stream_t stream) {
-    if (!guq || !sgu || !fg8h::aligned16(guq) || (reinterpret_cast<uintptr_t>(sgu) & 3))
+    if ((M_total != 0 && (!guq || !sgu)) || !fg8h::aligned16(guq) || (reinterpret_cast<uintptr_t>(sgu) & 3))
         return FG8_ERR_INVALID_ARG;
     return launch_swiglu(a, sa, b, sb, offsets, M_total, I, K, E, hq, sh, guq, sgu, dev_status, stream);
 }
@@ -1303,7 +1304,8 @@ extern "C" fg8_status fg8_grouped_gemm_combine(const uint8_t* a, const float* sa
                                                int normalize, float* out, void* workspace,
                                                size_t ws_bytes, int32_t* dev_status,
                                                fg8_stream_t stream) {
-    if (!a || !sa || !b || !sb || !offsets || !row_token || !token_row || !affinity || !out)
+    if ((M_total != 0 && (!a || !sa || !row_token)) || (T != 0 && (!token_row || !affinity || !out)) || !b || !sb ||
+        !offsets)
         return FG8_ERR_INVALID_ARG;
     if (E < 1 || N < 128 || K < 128 || N % 128 || K % 128 || M_total < 0 || T < 0)
         return FG8_ERR_INVALID_ARG;

@@ -237,6 +237,8 @@ fg8_status fg8_transpose_blockq(const uint8_t* wq, const float* sw, int E, int N
  *            [offsets[e], offsets[e+1]); offsets[E] <= M_total
  *   out      [M_total][N] bf16 or fp32; rows outside [0, offsets[E]) are
  *            not written.  An expert with no rows costs nothing.
+ *   M_total = 0 is no error, and the buffers of its rows (a, sa, out) may then be
+ *   NULL (in the gated up-projections hq, sh, guq and sgu too).
  *   N % 128 == 0, K % 128 == 0, E <= 1024.  workspace may be NULL.
  *
  * group_mode = FG8_GROUP_K (weight gradient; variable contraction per expert):

@@ -143,3 +143,19 @@ def test_left_out_dots_and_logits(L):
     with pytest.raises(ValueError, match="gate_dot"):
         fg8.swiglu_backward_quant(z(6, 128, dt=torch.bfloat16), z(6, 256), z(2, 6, dt=f32), z(2, dt=i32),
                                   gate_dot=z(2, 6, dt=f32), want_dots=False)
+
+
+def test_gemms_of_no_rows_take_no_row_buffers(L):
+    """An empty batch's buffers have no address; the weights and offsets are still looked at."""
+    swiglu = dict(a=None, sa=None, b=16, sb=16, offsets=16, M=0, I=128, K=128, E=1, hq=None, sh=None)
+    save = dict(swiglu, guq=None, sgu=None, st=None, stream=None)
+    swiglu.update(st=None, stream=None)
+    gemm = dict(a=None, sa=None, b=16, sb=16, offsets=16, M=0, N=128, K=128, E=1, mode=fg8.FG8_GROUP_M,
+                bmode=fg8.FG8_BSCALE_BLOCK128, dt=fg8.FG8_OUT_BF16, out=None, ws=None, n=0, st=None, stream=None)
+    combine = dict(a=None, sa=None, b=16, sb=16, offsets=16, M=0, N=128, K=128, E=1, rt=None, tr=None, aff=None, T=0,
+                   k=2, norm=1, out=None, ws=None, n=0, st=None, stream=None)
+    for f, good in ((L.fg8_grouped_gemm_swiglu_quant, swiglu), (L.fg8_grouped_gemm_swiglu_quant_save, save),
+                    (L.fg8_grouped_gemm, gemm), (L.fg8_grouped_gemm_combine, combine)):
+        _refused(f, good, [(OK, [{}]), (INV, [dict(b=None), dict(sb=None), dict(offsets=None), dict(E=0), dict(K=100)]),
+                           (INV, [dict(M=1), dict(M=-1)])])
+    _refused(L.fg8_grouped_gemm_combine, combine, [(INV, [dict(T=1), dict(T=1, tr=16, aff=16), dict(M=1, a=16, sa=16)])])

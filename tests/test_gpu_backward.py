@@ -667,3 +667,15 @@ def test_gate_backward_without_logits_is_the_same(normalize):
     got, none = fg8.gate_backward(dot, tr, None, aff, E, normalize=normalize, want_dlogits=False)
     torch.cuda.synchronize()
     assert none is None and dlogits is not None and torch.equal(got, want)
+
+
+def test_training_step_of_no_tokens():
+    """A rank whose batch is empty: every call of the step takes it, outputs of no rows
+    are empty and the weights' gradients are zeros."""
+    E, k, C, I = 3, 2, 256, 128
+    z = lambda *s: torch.randn(s, device="cuda").to(torch.bfloat16)   # noqa: E731
+    r = _step(z(0, C), torch.randn(0, E, device="cuda"), torch.zeros(E, device="cuda"), z(E, 2 * I, C), z(E, C, I),
+              z(0, C), k)
+    assert r["out"].shape == (0, C) and r["dx"].shape == (0, C) and r["dlogits"].shape == (0, E)
+    assert r["dwu"].shape == (E, 2 * I, C) and not r["dwu"].any()
+    assert r["dwd"].shape == (E, C, I) and not r["dwd"].any()
