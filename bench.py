@@ -164,16 +164,16 @@ TRAFFIC_CAPTURE = {
     "config": "dsv3",
     "fused_act": True,
     "families": {
-        "quant_act_permute": (598.5e6, "quant_act", "c5187dc2015d"),
+        "quant_act_permute": (598.5e6, "quant_act", "a0d2f796784c"),
         "quant_weight": (41280.4e6, "quant_weight", "c5689f11fc37"),
-        "gemm_fprop_up_swiglu_quant": (8051.9e6, "gemm", "c0082e7e4a78"),
-        "quant_act_rows": (777.8e6, "quant_act", "c5187dc2015d"),
-        "gemm_fprop_down": (4594.3e6, "gemm", "c0082e7e4a78"),
-        "gemm_dgrad": (8419.0e6, "gemm", "c0082e7e4a78"),
-        "quant_act_colwise": (1573.4e6, "quant_act", "c5187dc2015d"),
-        "gemm_wgrad": (31927.9e6, "gemm", "c0082e7e4a78"),
+        "gemm_fprop_up_swiglu_quant": (8245.8e6, "gemm", "66717c6bafe1"),
+        "quant_act_rows": (778.4e6, "quant_act", "a0d2f796784c"),
+        "gemm_fprop_down": (4594.6e6, "gemm", "66717c6bafe1"),
+        "gemm_dgrad": (8379.5e6, "gemm", "66717c6bafe1"),
+        "quant_act_colwise": (1574.3e6, "quant_act", "a0d2f796784c"),
+        "gemm_wgrad": (31918.2e6, "gemm", "66717c6bafe1"),
         "transpose_blockq": (14976.3e6, "transpose", "3f2c2c5f91b7"),
-        "gemm_fprop_up": (8555.7e6, "gemm", "c0082e7e4a78"),
+        "gemm_fprop_up": (8773.6e6, "gemm", "66717c6bafe1"),
         "unpermute_combine": (1044.5e6, "combine", "641810fdcb7b"),
     },
 }

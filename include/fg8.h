@@ -339,8 +339,9 @@ fg8_status fg8_grouped_gemm_swiglu_quant_save(const uint8_t* a, const float* sa,
  *     gate_dot[c][r] = sum over the columns of block c of dh h
  * so that, the layer's output being sum_j w_j Wd h_j, the sum of a row's
  * gate_dot over c is dL/dw (fg8_gate_backward).  Arithmetic in fp32 (fast
- * exponential and reciprocal: sig is off by at most (2 |g| + 8) 2^-24 of itself,
- * and 0 where it is below 2^-126; large gates lose nothing else).  Each tile's scale is fp32(amax / 448)
+ * exponential and reciprocal: for g = fp32(code * scale), sig is off by at most
+ * (2 |g| + 8) 2^-24 of itself, and 0 where it is below 2^-126; large gates lose
+ * nothing else).  Each tile's scale is fp32(amax / 448)
  * and its codes E4M3 (RNE, saturating) of the value times fp32(1 / scale),
  * i.e. of the quotient to within 2^-22.
  *   dh       bf16 [R][I]

@@ -136,6 +136,7 @@ def act_formula(oracle, c):
     h, d = g * sig * u, dh * w
     SIG = (2 * np.abs(g) + 8) * EPS
     # below exp(-125 ln 2) the kernel holds sig at 2^-125: that much absolutely
+    # (or lets it go to 0 below 2^-126, as it does now: within the same)
     floor = 2.0 ** -124
     dG, dU = d * u * sig * (1 + g * (1 - sig)), d * g * sig
     tG = (np.abs(d * u * sig) * ((1 + np.abs(g)) * (SIG + 4 * EPS)) + np.abs(dG) * (SIG + 5 * EPS)
