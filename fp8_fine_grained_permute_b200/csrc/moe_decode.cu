@@ -41,14 +41,16 @@
 // operand B (codes of x or h) and the scale products.
 //
 // On a B200 (and the share of the measured copy rate that the weights alone make):
-//   256 experts x 7168 x 2048, top 8: 1 token 69 us (0.79), 8 tokens 366 us (0.9 and
-//   more, by the experts met); 64 experts x 2048 x 768, top 6: 1 token 17.4 us (0.25),
-//   37 tokens 72 us (0.64).  The stream runs at HBM speed (a step's 32 KB an SM take
-//   0.68 us, its MMAs 0.6); the rest is the start (3 us for one token's routing
-//   and lists, 8 for 37 tokens), the meeting of all CTAs between the
-//   projections and the joins.  Measured on the way there: x quantized by every CTA
-//   for itself, flags and fences in the joins, unrolled code (39 us for the first of
-//   the 64-expert cases: instructions that run once are fetched cold).
+//   256 experts x 7168 x 2048, top 8: 1 token 69 us (0.79), 8 tokens 367 us (0.9 and
+//   more, by the experts met), 64 tokens 1136 us (0.98); 64 experts x 2048 x 768, top
+//   6: 1 token 17.3 us (0.25), 37 tokens 73 us (0.64).  The stream runs at HBM speed (a
+//   step's 32 KB an SM take 0.68 us, its MMAs 0.6).  What is around it, of 17.3 us at 64
+//   experts and 1 token: 2.5 until the lists stand (7 for 37 tokens), 3 more to the first
+//   product (x's codes from all CTAs, the first weights), 2 for the joins of h, 1.5 for
+//   the meeting, 1.5 to the first product after it, 1.5 for the joins of out, 1.8 for
+//   the launch and the end; the two streams take 1.75 each.  Measured on the way there: x
+//   quantized by every CTA for itself, flags and fences in the joins, unrolled code
+//   (39 us for this case: instructions that run once are fetched cold).
 // N = 16 for T <= 16: with N = 32 (a stage less, half of every product unused) the
 // same cases take 19.8 us, 75.0 us (256 experts, 1 token) and 369 us (8 tokens)
 // against 18.0, 68.2 and 359.  The router's registers an expert are cut to E: all
