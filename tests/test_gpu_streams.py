@@ -88,3 +88,22 @@ def test_output_is_not_in_memory_that_the_current_stream_still_uses(data, name, 
     side.synchronize()
     torch.cuda.synchronize()
     assert torch.equal(late, want)
+
+
+@pytest.mark.parametrize("name", CALLS)
+@pytest.mark.parametrize("handle", [False, True])
+def test_stream_named_inside_a_capture(data, name, handle):
+    """A capture whose calls name its own stream: what they allocate belongs to the graph."""
+    call = CALLS[name]
+    n = 128 if name == "requantize" else None
+    want = bits(call(data, None), n).clone()
+    s = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=s):
+        out = call(data, s.cuda_stream if handle else s)
+    for _ in range(2):
+        out.view(torch.uint8).fill_(0x5A)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(bits(out, n), want)
